@@ -185,8 +185,7 @@ def prepare(case, seed):
         if op == "step":
             st["k_new"], st["v_new"] = _bf16(g, B, hkv, DK), _bf16(g, B, hkv, DV)
             st["pos"], st["seq"] = st["lens"] - 1, torch.arange(B, dtype=torch.int32, device="cuda")
-        if own_workspace := _workspace_bytes(case, st["max_len"]):
-            st["workspace"] = torch.empty(own_workspace, dtype=torch.uint8, device="cuda")
+        st["workspace"] = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")  # a serving loop's scratch
         return st
     if op == "append":
         n = int(lens.sum())
@@ -238,15 +237,6 @@ def prepare(case, seed):
         st["k_out"] = torch.zeros((st["pages_out"], PAGE, 4, DK), dtype=st["k"].dtype, device="cuda")
         st["v_out"] = torch.zeros((st["pages_out"], PAGE, 4, DV), dtype=st["v"].dtype, device="cuda")
     return st
-
-
-def _workspace_bytes(case, max_len):
-    """Room for split-KV partials that a serving loop keeps: the library's own answer is at most
-    this (one partial of 16 query rows per 128 keys and row block, 128 + 2 floats a row)."""
-    if case["ring"]:
-        return 0
-    blocks = case["B"] * _kv_heads(case) * case["q_len"]
-    return min(blocks * (max_len // 128 + 2), 4096 + 2 * blocks) * 16 * 130 * 4 + 65536
 
 
 # ------------------------------------------------------------------------------------- plain form
@@ -471,7 +461,7 @@ def _own_decode(st):
         st["q"], st["lens"], max_seq_len=st["max_len"], num_kv_heads=_kv_heads(case),
         rope_base=SWA_BASE if ring else GLOBAL_BASE, window=ring - case["q_len"] + 1 if ring else 0,
         cache_kind=M.MIMO_CACHE_RING if ring else M.MIMO_CACHE_PAGED, k_cache=st["k"], v_cache=st["v"],
-        block_table=st["table"], num_pages=st["pages"], sink=st["sink"], workspace=st.get("workspace"),
+        block_table=st["table"], num_pages=st["pages"], sink=st["sink"], workspace=st["workspace"],
         cache_dtype=M.MIMO_DTYPE_INT4, ring_slots=ring, q_len=case["q_len"])
 
 
