@@ -29,6 +29,9 @@ MIMO_CACHE_PAGED = 1
 MIMO_CACHE_RING = 2
 MIMO_DTYPE_BF16 = 0
 MIMO_DTYPE_FP8_E4M3 = 1
+MIMO_DTYPE_INT4 = 2
+MIMO_INT4_K_SLOT_BYTES = 108
+MIMO_INT4_V_SLOT_BYTES = 72
 MIMO_RING_SLOTS_DEFAULT = 128
 MIMO_RING_SLOTS_MAX = 512
 MIMO_MAX_DRAFTS = 8
@@ -41,7 +44,8 @@ SOFTMAX_SCALE = 1.0 / math.sqrt(192.0)
 V_SCALE = 0.707
 
 EXPORTS = ("mimo_attn_prefill", "mimo_attn_prefill_workspace_size", "mimo_attn_prefill_stall_test", "mimo_attn_decode",
-           "mimo_attn_decode_workspace_size", "mimo_attn_verify_workspace_size", "mimo_attn_decode_noalloc",
+           "mimo_attn_decode_workspace_size", "mimo_attn_verify_workspace_size",
+           "mimo_attn_decode_int4_workspace_size", "mimo_attn_decode_noalloc",
            "mimo_kv_append", "mimo_last_error",
            "mimo_status_poll", "mimo_version", "mimo_window_from_left_right")
 DECODE_NOALLOC_MAX_BYTES = 16 << 20
@@ -71,7 +75,7 @@ class MimoDecodeArgs(C.Structure):
                 ("block_table", _P), ("max_pages", C.c_int), ("num_pages", C.c_int), ("out", _P), ("lse", _P),
                 ("workspace", _P), ("workspace_bytes", C.c_size_t), ("ev_kernel_begin", _P),
                 ("ev_kernel_end", _P), ("cache_dtype", C.c_int), ("k_dequant", _P), ("v_dequant", _P),
-                ("ring_slots", C.c_int), ("q_len", C.c_int)]
+                ("ring_slots", C.c_int), ("q_len", C.c_int), ("positions", _P)]
 
 
 class MimoAppendArgs(C.Structure):
@@ -80,7 +84,7 @@ class MimoAppendArgs(C.Structure):
                 ("v_new", _P), ("pos", _P), ("seq_idx", _P), ("cache_kind", C.c_int), ("k_cache", _P),
                 ("v_cache", _P), ("num_seqs", C.c_int), ("block_table", _P), ("max_pages", C.c_int),
                 ("num_pages", C.c_int), ("cache_dtype", C.c_int), ("k_dequant", _P), ("v_dequant", _P),
-                ("ring_slots", C.c_int)]
+                ("ring_slots", C.c_int), ("slots", _P)]
 
 
 _lib = None
@@ -112,6 +116,8 @@ def lib():
         L.mimo_attn_decode_workspace_size.restype = C.c_size_t
         L.mimo_attn_verify_workspace_size.argtypes = [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]
         L.mimo_attn_verify_workspace_size.restype = C.c_size_t
+        L.mimo_attn_decode_int4_workspace_size.argtypes = [C.c_int] * 6
+        L.mimo_attn_decode_int4_workspace_size.restype = C.c_size_t
         L.mimo_attn_decode_noalloc.argtypes = [C.POINTER(MimoDecodeArgs), _P]
         L.mimo_attn_decode_noalloc.restype = C.c_int
         L.mimo_kv_append.argtypes = [C.POINTER(MimoAppendArgs), _P]
@@ -158,7 +164,10 @@ def prefill_workspace_size(num_seqs: int, total_q: int, total_k: int, num_kv_hea
     return int(lib().mimo_attn_prefill_workspace_size(num_seqs, total_q, total_k, num_kv_heads, cache_kind))
 
 
-def decode_workspace_size(batch: int, max_seq_len: int, num_kv_heads: int, window: int, q_len: int = 1) -> int:
+def decode_workspace_size(batch: int, max_seq_len: int, num_kv_heads: int, window: int, q_len: int = 1,
+                          cache_dtype: int = MIMO_DTYPE_BF16, cache_kind: int = MIMO_CACHE_PAGED) -> int:
+    if cache_dtype == MIMO_DTYPE_INT4:
+        return int(lib().mimo_attn_decode_int4_workspace_size(batch, q_len, max_seq_len, num_kv_heads, window, cache_kind))
     if q_len == 1:
         return int(lib().mimo_attn_decode_workspace_size(batch, max_seq_len, num_kv_heads, window))
     return int(lib().mimo_attn_verify_workspace_size(batch, q_len, max_seq_len, num_kv_heads, window))
@@ -221,10 +230,13 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
                      cache_kind: int, k_cache, v_cache, block_table=None, num_pages: int = 0, sink=None, out=None,
                      lse=None, workspace=None, softmax_scale: float = SOFTMAX_SCALE, v_scale: float = V_SCALE,
                      stream=None, with_lse: bool = True, kernel_events=None, cache_dtype: int = MIMO_DTYPE_BF16,
-                     k_dequant=None, v_dequant=None, ring_slots: int = 0, q_len: int = 1):
+                     k_dequant=None, v_dequant=None, ring_slots: int = 0, q_len: int = 1, positions=None):
     """Decode step (see include/mimoattn.h).  kernel_events as for mimo_attn_prefill (around the
     split kernel, not the combine).  ring_slots: slots per sequence of a ring cache (0 = 128).
     q_len: query tokens per sequence (draft tokens to verify; q holds batch * q_len rows).
+    cache_dtype: MIMO_DTYPE_BF16, MIMO_DTYPE_FP8_E4M3 (with k_dequant / v_dequant) or
+    MIMO_DTYPE_INT4 (uint8 caches, see empty_int4_cache).  positions: int32 [batch] rotary
+    position of each sequence's last query token (None: seq_lens - 1), for evicted caches.
     Returns (out, lse)."""
     import torch
     rows = q.shape[0]
@@ -235,7 +247,7 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
         out = torch.empty((rows, NUM_Q_HEADS, HEAD_DIM_V), dtype=torch.bfloat16, device=q.device)
     if lse is None and with_lse:
         lse = torch.empty((rows, NUM_Q_HEADS), dtype=torch.float32, device=q.device)
-    need = decode_workspace_size(B, max_seq_len, num_kv_heads, window, q_len)
+    need = decode_workspace_size(B, max_seq_len, num_kv_heads, window, q_len, cache_dtype, cache_kind)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     a = MimoDecodeArgs()
@@ -252,6 +264,7 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
     a.ev_kernel_begin, a.ev_kernel_end = _events(kernel_events)
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
     a.ring_slots, a.q_len = int(ring_slots), int(q_len)
+    a.positions = _ptr(positions)
     _check(lib().mimo_attn_decode(C.byref(a), _stream(stream)))
     return out, lse
 
@@ -280,10 +293,12 @@ def mimo_attn_decode_noalloc(q, seq_lens, *, max_seq_len: int, num_kv_heads: int
 
 def mimo_kv_append(k_new, v_new, pos, seq_idx, *, rope_base: float, cache_kind: int, k_cache, v_cache,
                    num_seqs: int, block_table=None, num_pages: int = 0, stream=None,
-                   cache_dtype: int = MIMO_DTYPE_BF16, k_dequant=None, v_dequant=None, ring_slots: int = 0):
+                   cache_dtype: int = MIMO_DTYPE_BF16, k_dequant=None, v_dequant=None, ring_slots: int = 0,
+                   slots=None):
     """Rotate and store new keys/values into the ring or paged cache (see include/mimoattn.h);
-    an E4M3 cache (cache_dtype) quantises with the per-KV-head scales k_dequant / v_dequant.
-    ring_slots: slots per sequence of a ring cache (0 = 128)."""
+    an E4M3 cache (cache_dtype) quantises with the per-KV-head scales k_dequant / v_dequant, a
+    4-bit cache with scales of its own.  ring_slots: slots per sequence of a ring cache (0 =
+    128).  slots: int32 [tokens] cache slot of each token where it is not pos (paged caches)."""
     a = MimoAppendArgs()
     a.num_tokens, a.num_kv_heads = k_new.shape[0], k_new.shape[1]
     a.head_dim_qk, a.head_dim_v, a.rope_dim, a.rope_base = HEAD_DIM_QK, HEAD_DIM_V, ROPE_DIM, float(rope_base)
@@ -295,8 +310,17 @@ def mimo_kv_append(k_new, v_new, pos, seq_idx, *, rope_base: float, cache_kind: 
     a.max_pages = 0 if block_table is None else block_table.shape[1]
     a.num_pages = num_pages
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
-    a.ring_slots = int(ring_slots)
+    a.ring_slots, a.slots = int(ring_slots), _ptr(slots)
     _check(lib().mimo_kv_append(C.byref(a), _stream(stream)))
+
+
+def empty_int4_cache(blocks: int, num_kv_heads: int, ring_slots: int = 0, device="cuda"):
+    """Zeroed (k_cache, v_cache) of a 4-bit cache: `blocks` pages of 128 slots, or (ring_slots > 0)
+    `blocks` sequences' rings; uint8 [blocks, num_kv_heads, slots * bytes per slot]."""
+    import torch
+    n = ring_slots or 128
+    return tuple(torch.zeros((blocks, num_kv_heads, n * b), dtype=torch.uint8, device=device)
+                 for b in (MIMO_INT4_K_SLOT_BYTES, MIMO_INT4_V_SLOT_BYTES))
 
 
 def mimo_window_from_left_right(left: int, right: int = 0) -> int:

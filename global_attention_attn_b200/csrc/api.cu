@@ -168,8 +168,10 @@ int get_encoder(const char* fn, EncodeTiledFn* out) {
 // 3-D bf16 tensor [rows, heads, dim] (dim innermost) with box {64, box_h, box_rows},
 // 128-byte swizzle, zero fill out of bounds.
 int check_cache_dtype(const char* fn, int dtype, const float* kdq, const float* vdq) {
-  if (dtype != MIMO_DTYPE_BF16 && dtype != MIMO_DTYPE_FP8_E4M3)
+  if (dtype != MIMO_DTYPE_BF16 && dtype != MIMO_DTYPE_FP8_E4M3 && dtype != MIMO_DTYPE_INT4)
     return fail(MIMO_ERR_INVALID_ARG, "%s: unknown cache_dtype %d", fn, dtype);
+  if (dtype == MIMO_DTYPE_INT4 && (kdq || vdq))
+    return fail(MIMO_ERR_INVALID_ARG, "%s: a 4-bit cache holds its scales: k_dequant / v_dequant must be NULL", fn);
   if (dtype == MIMO_DTYPE_FP8_E4M3) {
     if (!kdq || !vdq) return fail(MIMO_ERR_INVALID_ARG, "%s: an E4M3 cache needs k_dequant and v_dequant", fn);
     if ((reinterpret_cast<uintptr_t>(kdq) | reinterpret_cast<uintptr_t>(vdq)) & 3)
@@ -221,6 +223,91 @@ size_t decode_workspace(int batch, int q_len, int max_seq_len, int window) {
   if (ns <= 1) return 0;
   const size_t rows = size_t(batch) * q_len;
   return round256(rows * kHq * ns * kDv * 4) + round256(rows * kHq * ns * 2 * 4);
+}
+
+// Segments of a 4-bit decode's workers, and the tile table its combine reads.
+size_t decode4_workspace(const Decode4Plan& d, int batch) {
+  if (d.whole_units) return 0;
+  const size_t rows = 2 * size_t(d.workers) * d.n_blocks * 16;
+  return round256(rows * kDv * 4) + round256(rows * 2 * 4) +
+         round256((size_t(batch < kI4MaxBatch ? batch : kI4MaxBatch) + 1) * 8);
+}
+// The plan never counts on more SMs than this, so that the size query needs no device.
+constexpr int kI4Sms = 148;
+
+// mimo_attn_decode on a 4-bit cache, after its checks.
+int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_slots, size_t room, void* stream) {
+  DevState d;
+  if (int rc = dev_state(fn, &d)) return rc;
+  EncodeTiledFn enc;
+  if (int rc = get_encoder(fn, &enc)) return rc;
+  const bool ring = a->cache_kind == MIMO_CACHE_RING;
+  const int hkv = a->layer.num_kv_heads;
+  Decode4Params p;
+  std::memset(&p, 0, sizeof(p));
+  Decode4Plan plan = decode4_plan(a->batch < kI4MaxBatch ? a->batch : kI4MaxBatch, hkv, q_len,
+                                  ring ? ring_slots : decode_unit_keys(a->max_seq_len, a->layer.window, q_len), ring,
+                                  d.sms < kI4Sms ? d.sms : kI4Sms);
+  while (plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
+  {
+    const cuuint64_t slots = ring ? ring_slots : kPage;
+    const cuuint64_t blocks = cuuint64_t(ring ? a->batch : a->num_pages) * hkv;
+    cuuint64_t gdim[3] = {64, slots, blocks};
+    cuuint64_t gstride[2] = {64, slots * MIMO_INT4_V_SLOT_BYTES};
+    cuuint32_t box[3] = {64, kI4Tile, 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = enc(&p.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a->v_cache), gdim, gstride, box,
+                     estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MIMO_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", fn, int(r));
+  }
+  p.hkv = hkv;
+  p.group = kHq / hkv;
+  p.q_len = q_len;
+  p.n_blocks = plan.n_blocks;
+  p.nc = plan.nc;
+  p.groups = plan.groups;
+  p.stages = plan.stages;
+  p.workers = plan.workers;
+  p.min_tiles = plan.min_tiles;
+  p.whole_units = plan.whole_units;
+  p.window = a->layer.window;
+  p.max_seq_len = a->max_seq_len;
+  p.scale_log2 = a->layer.softmax_scale * 1.4426950408889634f;
+  p.v_scale = a->layer.v_scale;
+  p.sink = a->layer.sink;
+  p.cache_kind = a->cache_kind;
+  p.ring_slots = ring_slots;
+  p.max_pages = a->max_pages;
+  p.num_pages = a->num_pages;
+  p.rope = make_freqs(a->layer.rope_base);
+  p.status = d.status;
+  if (!plan.whole_units) {
+    char* ws = static_cast<char*>(a->workspace);
+    const size_t rows = 2 * size_t(plan.workers) * plan.n_blocks * 16;
+    p.ws_o = reinterpret_cast<float*>(ws);
+    p.ws_ml = reinterpret_cast<float*>(ws + round256(rows * kDv * 4));
+    p.ws_tbl = reinterpret_cast<long long*>(ws + round256(rows * kDv * 4) + round256(rows * 2 * 4));
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // launches of at most kI4MaxBatch sequences, which follow each other on the stream and share
+  // the workspace
+  for (int s0 = 0; s0 < a->batch; s0 += kI4MaxBatch) {
+    p.batch = a->batch - s0 < kI4MaxBatch ? a->batch - s0 : kI4MaxBatch;
+    p.q = static_cast<const uint16_t*>(a->q) + long(s0) * q_len * kHq * kDqk;
+    p.seq_lens = a->seq_lens + s0;
+    p.positions = a->positions ? a->positions + s0 : nullptr;
+    p.block_table = a->block_table ? a->block_table + long(s0) * a->max_pages : nullptr;
+    p.k_cache = static_cast<const uint8_t*>(a->k_cache);
+    p.v_cache = static_cast<const uint8_t*>(a->v_cache);
+    p.block0 = ring ? long(s0) * hkv : 0;
+    p.out = static_cast<uint16_t*>(a->out) + long(s0) * q_len * kHq * kDv;
+    p.lse = a->lse ? a->lse + long(s0) * q_len * kHq : nullptr;
+    const bool last = s0 + kI4MaxBatch >= a->batch;
+    cudaError_t e = launch_decode4(p, d.sms, st, s0 == 0 ? a->ev_kernel_begin : nullptr, last ? a->ev_kernel_end : nullptr);
+    if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  }
+  return MIMO_OK;
 }
 
 // Draft verification of a global layer on a bf16 paged cache: the q_len rows of a sequence's 16
@@ -356,6 +443,16 @@ size_t mimo_attn_verify_workspace_size(int batch, int q_len, int max_seq_len, in
   return decode_workspace(batch, q_len, max_seq_len, window);
 }
 
+size_t mimo_attn_decode_int4_workspace_size(int batch, int q_len, int max_seq_len, int num_kv_heads, int window,
+                                            int cache_kind) {
+  if (batch <= 0 || max_seq_len <= 0 || q_len < 1 || q_len > MIMO_MAX_DRAFTS || (num_kv_heads != 8 && num_kv_heads != 4) ||
+      window < 0 || cache_kind != MIMO_CACHE_PAGED)
+    return 0;
+  return decode4_workspace(decode4_plan(batch < kI4MaxBatch ? batch : kI4MaxBatch, num_kv_heads, q_len,
+                                        decode_unit_keys(max_seq_len, window, q_len), false, kI4Sms),
+                           batch);
+}
+
 int mimo_kv_append(const mimo_append_args* a, void* stream) {
   const char* fn = "mimo_kv_append";
   if (!a) return fail(MIMO_ERR_INVALID_ARG, "%s: args is NULL", fn);
@@ -384,6 +481,11 @@ int mimo_kv_append(const mimo_append_args* a, void* stream) {
   if (int rc = check_cache_dtype(fn, a->cache_dtype, a->k_dequant, a->v_dequant)) return rc;
   int ring_slots = 0;
   if (int rc = ring_slots_of(fn, a->ring_slots, &ring_slots)) return rc;
+  if (a->slots) {
+    REQUIRE_PTR(a->slots, "slots");
+    if (a->cache_kind == MIMO_CACHE_RING)
+      return fail(MIMO_ERR_INVALID_ARG, "%s: slots needs a paged cache (a ring's slots follow from pos)", fn);
+  }
   DevState d;
   if (int rc = dev_state(fn, &d)) return rc;
   AppendParams p;
@@ -394,6 +496,7 @@ int mimo_kv_append(const mimo_append_args* a, void* stream) {
   p.v_new = static_cast<const uint16_t*>(a->v_new);
   p.pos = a->pos;
   p.seq_idx = a->seq_idx;
+  p.slots = a->slots;
   p.cache_kind = a->cache_kind;
   p.k_cache = static_cast<uint16_t*>(a->k_cache);
   p.v_cache = static_cast<uint16_t*>(a->v_cache);
@@ -402,6 +505,7 @@ int mimo_kv_append(const mimo_append_args* a, void* stream) {
   p.max_pages = a->max_pages;
   p.num_pages = a->num_pages;
   p.fp8 = a->cache_dtype == MIMO_DTYPE_FP8_E4M3;
+  p.int4 = a->cache_dtype == MIMO_DTYPE_INT4;
   p.k_dequant = a->k_dequant;
   p.v_dequant = a->v_dequant;
   p.rope = make_freqs(a->rope_base);
@@ -411,8 +515,13 @@ int mimo_kv_append(const mimo_append_args* a, void* stream) {
   return MIMO_OK;
 }
 
-int mimo_attn_decode(const mimo_decode_args* a, void* stream) {
-  const char* fn = "mimo_attn_decode";
+}  // extern "C"
+
+namespace mimo {
+namespace {
+
+// cut_to_fit: a 4-bit decode takes no more pieces than the workspace holds (the no-alloc call)
+int decode_impl(const char* fn, const mimo_decode_args* a, void* stream, bool cut_to_fit) {
   if (!a) return fail(MIMO_ERR_INVALID_ARG, "%s: args is NULL", fn);
   if (int rc = check_layer(fn, a->layer)) return rc;
   if (a->batch < 0) return fail(MIMO_ERR_INVALID_ARG, "%s: batch must be >= 0", fn);
@@ -447,15 +556,26 @@ int mimo_attn_decode(const mimo_decode_args* a, void* stream) {
       return fail(MIMO_ERR_INVALID_ARG, "%s: max_pages * 128 is below max_seq_len", fn);
   }
   if (int rc = check_cache_dtype(fn, a->cache_dtype, a->k_dequant, a->v_dequant)) return rc;
-  const size_t need = decode_workspace(a->batch, q_len, a->max_seq_len, a->layer.window);
+  if (a->positions) {
+    REQUIRE_PTR(a->positions, "positions");
+    if (a->cache_kind == MIMO_CACHE_RING || a->layer.window > 0)
+      return fail(MIMO_ERR_INVALID_ARG, "%s: positions needs a paged cache and no window", fn);
+  }
+  const bool int4 = a->cache_dtype == MIMO_DTYPE_INT4;
+  const size_t need = int4 ? (cut_to_fit ? 0
+                                         : mimo_attn_decode_int4_workspace_size(a->batch, q_len, a->max_seq_len,
+                                                                                a->layer.num_kv_heads, a->layer.window,
+                                                                                a->cache_kind))
+                           : decode_workspace(a->batch, q_len, a->max_seq_len, a->layer.window);
   if (need > 0) {
     if (!a->workspace || a->workspace_bytes < need)
       return fail(MIMO_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", fn, need,
                   a->workspace ? a->workspace_bytes : size_t(0));
     if (!aligned16(a->workspace)) return fail(MIMO_ERR_INVALID_ARG, "%s: workspace is not 16-byte aligned", fn);
   }
+  if (int4) return decode_int4(fn, a, q_len, ring_slots, cut_to_fit ? a->workspace_bytes : need, stream);
   if (q_len >= 2 && a->cache_kind == MIMO_CACHE_PAGED && a->cache_dtype != MIMO_DTYPE_FP8_E4M3 &&
-      a->layer.window <= 0 && a->layer.num_kv_heads == 4)
+      a->layer.window <= 0 && a->layer.num_kv_heads == 4 && !a->positions)
     return decode_drafts_paged_tc(fn, a, q_len, stream);
   DevState d;
   if (int rc = dev_state(fn, &d)) return rc;
@@ -493,6 +613,7 @@ int mimo_attn_decode(const mimo_decode_args* a, void* stream) {
   p.sink = a->layer.sink;
   p.q = static_cast<const uint16_t*>(a->q);
   p.seq_lens = a->seq_lens;
+  p.positions = a->positions;
   p.cache_kind = a->cache_kind;
   p.ring_slots = ring_slots;
   p.k_cache = static_cast<const uint16_t*>(a->k_cache);
@@ -515,12 +636,6 @@ int mimo_attn_decode(const mimo_decode_args* a, void* stream) {
   if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return MIMO_OK;
 }
-
-}  // extern "C"
-
-namespace mimo {
-namespace {
-
 
 int prefill_impl(const char* fn, const mimo_prefill_args* a, void* stream, unsigned long long wait_ns,
                  int withhold_q) {
@@ -710,6 +825,10 @@ int prefill_impl(const char* fn, const mimo_prefill_args* a, void* stream, unsig
 
 extern "C" {
 
+int mimo_attn_decode(const mimo_decode_args* a, void* stream) {
+  return decode_impl("mimo_attn_decode", a, stream, false);
+}
+
 int mimo_attn_prefill(const mimo_prefill_args* a, void* stream) {
   return prefill_impl("mimo_attn_prefill", a, stream, kWaitNs, 0);
 }
@@ -728,7 +847,7 @@ extern "C" {
 int mimo_attn_decode_noalloc(const mimo_decode_args* a, void* stream) {
   const char* fn = "mimo_attn_decode_noalloc";
   if (!a) return fail(MIMO_ERR_INVALID_ARG, "%s: args is NULL", fn);
-  if (a->batch > 0 && a->max_seq_len > 0) {
+  if (a->batch > 0 && a->max_seq_len > 0 && a->cache_dtype != MIMO_DTYPE_INT4) {
     const size_t need = decode_workspace(a->batch, a->q_len == 0 ? 1 : a->q_len, a->max_seq_len, a->layer.window);
     if (need > MIMO_DECODE_NOALLOC_MAX_BYTES)
       return fail(MIMO_ERR_WORKSPACE,
@@ -746,7 +865,7 @@ int mimo_attn_decode_noalloc(const mimo_decode_args* a, void* stream) {
     b.workspace = d.scratch;
     b.workspace_bytes = MIMO_DECODE_NOALLOC_MAX_BYTES;
   }
-  return mimo_attn_decode(&b, stream);
+  return decode_impl("mimo_attn_decode", &b, stream, true);
 }
 
 int mimo_status_poll(uint32_t* status) {

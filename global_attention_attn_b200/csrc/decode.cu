@@ -335,9 +335,10 @@ __global__ void __launch_bounds__(DecodeLayout<FP8, NC>::kThreads, 1)
         // one row per draft of the unit's blocks, padding drafts included (finite angles for
         // the rows that only fill a block)
         const int n_cs = NC == 1 ? 1 : p.n_blocks * rows_per_block;
+        const int pos0 = (p.positions ? p.positions[U.s] + 1 : U.ctx) - p.q_len;
         for (int i = 0; i < n_cs; ++i) {
           float c, s;
-          rope_cos_sin(U.ctx - p.q_len + i, p.rope.inv_freq[lane], &c, &s);
+          rope_cos_sin(pos0 + i, p.rope.inv_freq[lane], &c, &s);
           csr[i * 32 + lane] = make_float2(c, s);
         }
         if (lane == 0) *I = U;

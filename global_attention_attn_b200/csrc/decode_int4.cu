@@ -1,0 +1,648 @@
+// Decode and draft verification over a 4-bit cache (ring or paged): the attention of decode.cu
+// on the cache format of int4.cuh.
+//
+// 180 bytes per (key, KV head) stand against 16 x 320 multiply-adds (a global layer's 16 query
+// heads), 57 FLOP per byte, and every element has to be unpacked first: unlike the wide caches
+// this one is bound by instruction issue and mma.sync, and the kernel is laid out to spend as
+// few instructions per element as it can:
+//   - unpacking is one shift and four ANDs per 8 elements (int4.cuh); the key offset is the
+//     start value of a group's accumulator, and a group's scale multiplies its 16 x 8 products
+//     in fp32 (packed pairs), not its 32 x 8 elements;
+//   - a value's scale is moved into the probabilities (fp16 pairs), its transposed fragments
+//     come from ldmatrix.trans: a 16-bit element of the transposed matrix is 4 dims of a key,
+//     so a register is 4 dims of a key pair, ready for the same masks;
+//   - the value offset is one more product per group of dims, p against a constant.  A sum of
+//     p * code over tens of thousands of keys would grow far above the result and lose it to
+//     the accumulator's rounding; so the odd key of each pair enters as -p * (15 - code) (the
+//     complement is free in the mask's LOP3) and the sum stays near zero on the way.
+//
+// Workers are groups of nc warps (one per 16-row block of query rows, sharing the tiles).  The
+// tiles (32 keys) of all sequences and KV heads form one line, cut into as many equal pieces
+// as there are workers, so any mix of lengths loads every SM alike; a piece's first and last
+// (sequence, head) may be partial and go through the combine kernel, the others write their
+// rows directly.  Ring caches and short contexts are cut between (sequence, head) units only
+// and need no second kernel.  Each group's leader warp issues the copies of later tiles itself
+// (one bulk copy for the codes and for the scales, one TMA tile with the 64-byte swizzle for
+// the values); there are no producer warps, so all 8 warps multiply.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "int4.cuh"
+#include "ptx.cuh"
+#include "../../include/mimoattn.h"
+
+namespace mimo {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = kI4Tile;
+// stage: value codes (64-byte swizzle), key codes, key scales, value scales
+constexpr int kOffK = kTile * kI4VCodes, kOffKs = kOffK + kTile * kI4KCodes;
+constexpr int kOffVs = kOffKs + kTile * 2 * kI4KGroups;
+constexpr int kStage = 6144;
+static_assert(kOffVs + kTile * 2 * kI4VGroups <= kStage && kStage % 1024 == 0, "stage layout");
+constexpr int kAllStages = 32;
+constexpr int kOffBar = kAllStages * kStage;
+constexpr int kOffTbl = kOffBar + 2 * kAllStages * 8 + 16;
+constexpr int kSmem = kOffTbl + (kI4MaxBatch + 1) * 8 + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// probabilities are kept as 2^kPBias * p: products with small value scales stay clear of
+// fp16's subnormals (and 2^6 * 1023, the largest scale an append stores, below its limit)
+constexpr float kPBias = 6.f;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
+}
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* r) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Keys a sequence's unit covers: [lo, end), and its first tile and tile count.
+struct Span {
+  int lo, end, t0, nt;
+};
+__device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
+  Span u;
+  u.end = p.cache_kind == MIMO_CACHE_RING ? ctx : min(ctx, p.max_seq_len);
+  u.lo = p.window > 0 ? max(0, ctx - p.q_len + 1 - p.window) : 0;
+  if (ctx < p.q_len || u.lo >= u.end) {
+    u.t0 = u.nt = 0;
+  } else if (p.cache_kind == MIMO_CACHE_RING) {
+    u.t0 = 0;
+    u.nt = (p.ring_slots + kTile - 1) / kTile;
+  } else {
+    u.t0 = u.lo / kTile;
+    u.nt = (u.end - 1) / kTile - u.t0 + 1;
+  }
+  return u;
+}
+
+// The line of tiles: sequence s's heads hold hkv * (tbl[s + 1] - tbl[s]) of them.  A position
+// on it, resolved.
+struct Cursor {
+  int s, g, t, nt;
+};
+__device__ __forceinline__ Cursor cursor_at(const long long* tbl, int batch, int hkv, long long x) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tbl[mid] * hkv <= x) lo = mid;
+    else hi = mid;
+  }
+  Cursor c;
+  c.s = lo;
+  c.nt = int(tbl[lo + 1] - tbl[lo]);
+  const long long rem = x - tbl[lo] * hkv;
+  c.g = int(rem / c.nt);
+  c.t = int(rem - (long long)c.g * c.nt);
+  return c;
+}
+// The next unit that has tiles (the caller knows there is one).
+__device__ __forceinline__ void next_unit(const long long* tbl, int hkv, Cursor& c) {
+  c.t = 0;
+  if (++c.g < hkv) return;
+  c.g = 0;
+  do {
+    ++c.s;
+    c.nt = int(tbl[c.s + 1] - tbl[c.s]);
+  } while (c.nt == 0);
+}
+
+// Workers that get a piece, and where a piece begins.
+__device__ __forceinline__ int workers_of(const Decode4Params& p, long long total) {
+  const long long w = (total + p.min_tiles - 1) / p.min_tiles;
+  return int(w < p.workers ? w : p.workers);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_constant__ Decode4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nc = p.nc, stages = p.stages;
+  const int grp = warp / nc, blk = warp - grp * nc;
+  const uint32_t ring0 = sbase + grp * stages * kStage;
+  const uint32_t bar0 = sbase + kOffBar + grp * stages * 16;
+  auto full = [&](int i) { return bar0 + 16 * i; };
+  auto empty = [&](int i) { return bar0 + 16 * i + 8; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 2 * kAllStages * 8);
+  long long* tbl = reinterpret_cast<long long*>(smem + kOffTbl);
+  if (grp < p.groups && blk == 0 && lane == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), nc);
+    }
+    if (grp == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarps - 1) {
+    long long carry = 0;
+    if (lane == 0) tbl[0] = 0;
+    for (int base = 0; base < p.batch; base += 32) {
+      const int s = base + lane;
+      long long n = 0;
+      if (s < p.batch) {
+        const int ctx = p.seq_lens[s];
+        if (ctx < p.q_len || (ctx > p.max_seq_len && p.cache_kind != MIMO_CACHE_RING))
+          atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+        n = span_of(p, ctx).nt;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n += u;
+      }
+      if (s < p.batch) tbl[s + 1] = carry + n;
+      carry += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (blockIdx.x == 0 && p.ws_tbl) {
+      __syncwarp();
+      for (int s = lane; s <= p.batch; s += 32) p.ws_tbl[s] = tbl[s];
+    }
+  }
+  __syncthreads();
+  if (grp >= p.groups) return;
+  const long long total = tbl[p.batch] * p.hkv;
+  if (total == 0) return;
+  const int w = grp * gridDim.x + blockIdx.x;
+  long long a, b;
+  if (p.whole_units) {
+    // pieces of whole (sequence, head) units
+    const long long units = (long long)p.batch * p.hkv;
+    const int W = int(units < p.workers ? units : p.workers);
+    if (w >= W) return;
+    auto at = [&](long long u) {
+      const int s = int(u / p.hkv);
+      return s >= p.batch ? total : tbl[s] * p.hkv + (u - (long long)s * p.hkv) * (tbl[s + 1] - tbl[s]);
+    };
+    a = at(w * units / W);
+    b = at((w + 1) * units / W);
+  } else {
+    const int W = workers_of(p, total);
+    if (w >= W) return;
+    a = w * total / W;
+    b = (w + 1) * total / W;
+  }
+  if (a >= b) return;
+
+  const bool leader = blk == 0;
+  const bool ring = p.cache_kind == MIMO_CACHE_RING;
+  const int slots = ring ? p.ring_slots : kPage;  // of a block
+  auto wait_w = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, MIMO_STATUS_TIMEOUT));
+  };
+
+  // ---- the leader's side: copies of the tiles a .. b - 1 in order
+  const Cursor start = cursor_at(tbl, p.batch, p.hkv, a);
+  Cursor ic = start;
+  long long issued = a;
+  int ist = 0, iph = 0;         // stage and pass of the next copy
+  int pg_s = -1, pg_base = 0, pg = 0, it0 = 0;  // lane i: page id of page pg_base + i of sequence pg_s
+  auto issue = [&]() -> bool {
+    if (issued >= b) return true;
+    if (ic.t == ic.nt) next_unit(tbl, p.hkv, ic);
+    long block;
+    int slot;
+    if (ring) {
+      block = p.block0 + long(ic.s) * p.hkv + ic.g;
+      slot = ic.t * kTile;
+    } else {
+      if (ic.s != pg_s) it0 = span_of(p, p.seq_lens[ic.s]).t0;
+      const int key = (it0 + ic.t) * kTile, pi = key / kPage;
+      if (ic.s != pg_s || pi < pg_base || pi >= pg_base + 32) {
+        pg_s = ic.s;
+        pg_base = pi;
+        const int last = (it0 + ic.nt - 1) * kTile / kPage, mine = pi + lane;
+        pg = 0;
+        if (mine <= last) {
+          pg = mine < p.max_pages ? p.block_table[long(ic.s) * p.max_pages + mine] : -1;
+          if (pg < 0 || pg >= p.num_pages) {
+            atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+            pg = 0;
+          }
+        }
+      }
+      block = long(__shfl_sync(0xffffffffu, pg, pi - pg_base)) * p.hkv + ic.g;
+      slot = key % kPage;
+    }
+    if (nc > 1 && iph > 0 && !wait_w(empty(ist), (iph - 1) & 1)) return false;
+    const int n = min(kTile, slots - slot);
+    const uint32_t dst = ring0 + ist * kStage, bar = full(ist);
+    if (lane == 0) {
+      mbar_expect_tx(bar, n * (kI4KSlot + 2 * kI4VGroups) + kTile * kI4VCodes);
+      const uint8_t* kb = p.k_cache + block * (long(slots) * kI4KSlot);
+      const uint8_t* vb = p.v_cache + block * (long(slots) * kI4VSlot);
+      bulk_load(dst + kOffK, kb + slot * kI4KCodes, n * kI4KCodes, bar);
+      bulk_load(dst + kOffKs, kb + slots * kI4KCodes + slot * 2 * kI4KGroups, n * 2 * kI4KGroups, bar);
+      bulk_load(dst + kOffVs, vb + slots * kI4VCodes + slot * 2 * kI4VGroups, n * 2 * kI4VGroups, bar);
+      tma_load_3d(dst, &p.tm_v, bar, 0, slot, int(block));
+    }
+    __syncwarp();
+    ++ic.t;
+    ++issued;
+    if (++ist == stages) ist = 0, ++iph;
+    return true;
+  };
+  // before the group leaves on a failed wait: let the copies under way land
+  auto drain = [&]() {
+    if (!leader || lane != 0) return;
+    int dummy = 0, st = ist, ph = iph;
+    for (int i = 0; i < stages && (ph > 0 || st > 0); ++i) {
+      if (--st < 0) st = stages - 1, --ph;
+      mbar_wait(full(st), ph & 1, &dummy, nullptr, 0, 50000000ull);
+    }
+  };
+  bool ok = true;
+  if (leader)
+    for (int i = 0; i < stages && ok; ++i) ok = issue();
+
+  // ---- every warp's side
+  const int q4 = lane & 3, r0 = lane >> 2;
+  const int G = p.group, rows = p.n_blocks * 16;
+  int st = 0, ph = 0;
+  bool behind = false;  // nc > 1: a stage was released but its next copy is not issued yet
+  Cursor c = start;
+  for (long long x = a; x < b && ok;) {
+    if (c.t == c.nt) next_unit(tbl, p.hkv, c);
+    const int s = c.s, g = c.g, t_first = c.t;
+    const int t_end = int(min((long long)c.nt, c.t + (b - x)));
+    const int ctx = p.seq_lens[s];
+    const Span U = span_of(p, ctx);
+    // rows r0 and r0 + 8 of the block: row 16 blk + r is draft (16 blk + r) / G
+    int lo_r[2], hi_r[2], draft[2];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      draft[hf] = (blk * 16 + 8 * hf) / G;
+      const int at = ctx - p.q_len + draft[hf];
+      // (a padding row sees what the row before it sees: it calls for no mask of its own)
+      const bool valid = draft[hf] < p.q_len;
+      lo_r[hf] = valid ? (p.window > 0 ? max(0, at - p.window + 1) : 0) : lo_r[0];
+      hi_r[hf] = valid ? min(U.end - 1, at) : hi_r[0];
+    }
+    // ---- query fragments and the key accumulators' start values
+    uint32_t qa[2 * kI4KGroups][4];
+    float ck[kI4KGroups][2];
+    {
+      float cs[2], sn[2];
+      const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (hf == 0 || draft[1] != draft[0]) {
+          rope_cos_sin(pos0 + draft[hf], p.rope.inv_freq[lane], &cs[hf], &sn[hf]);
+        } else {
+          cs[1] = cs[0];
+          sn[1] = sn[0];
+        }
+      }
+      uint4 raw[2][kI4KGroups];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int rr = blk * 16 + r0 + 8 * hf;
+        const bool valid = draft[hf] < p.q_len;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + ((long(s) * p.q_len + (valid ? draft[hf] : 0)) * kHq + g * G + rr % G) * kDqk + 8 * q4);
+#pragma unroll
+        for (int j = 0; j < kI4KGroups; ++j) raw[hf][j] = valid ? __ldg(src + 4 * j) : make_uint4(0, 0, 0, 0);
+      }
+      float amax = 0.f;
+      float v[2][2][8];  // [row][group 0 / 1][dim]
+      auto widen = [](const uint4& r, float* f) {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = lo_bf16(u[i]);
+          f[2 * i + 1] = hi_bf16(u[i]);
+        }
+      };
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        widen(raw[hf][0], v[hf][0]);
+        widen(raw[hf][1], v[hf][1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // dims 8 q4 + i and 32 + 8 q4 + i turn with frequency 8 q4 + i
+          const float ci = __shfl_sync(0xffffffffu, cs[hf], 8 * q4 + i), si = __shfl_sync(0xffffffffu, sn[hf], 8 * q4 + i);
+          const float xx = v[hf][0][i], yy = v[hf][1][i];
+          v[hf][0][i] = xx * ci - yy * si;
+          v[hf][1][i] = yy * ci + xx * si;
+        }
+      }
+      int4_query_group(v[0][0], v[1][0], qa, ck[0][0], ck[0][1], amax);
+      int4_query_group(v[0][1], v[1][1], qa + 2, ck[1][0], ck[1][1], amax);
+#pragma unroll
+      for (int j = 2; j < kI4KGroups; ++j) {
+        widen(raw[0][j], v[0][0]);
+        widen(raw[1][j], v[1][0]);
+        int4_query_group(v[0][0], v[1][0], qa + 2 * j, ck[j][0], ck[j][1], amax);
+      }
+      if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
+    }
+    const float c_log2 = p.scale_log2 * kI4KeyUnit;
+    const int R = p.ring_slots;
+    const int ring_off = ring ? ((R - ctx) % R + R) % R : 0;  // slot j holds position ctx - R + (j + ring_off) % R
+    const int lo_all = max(lo_r[0], lo_r[1]), hi_all = min(hi_r[0], hi_r[1]);
+    float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
+    float o[kI4VGroups][4][4], T[kI4VGroups][4];
+#pragma unroll
+    for (int u = 0; u < kI4VGroups; ++u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[u][e][0] = o[u][e][1] = o[u][e][2] = o[u][e][3] = 0.f;
+      T[u][0] = T[u][1] = T[u][2] = T[u][3] = 0.f;
+    }
+
+    for (; c.t < t_end; ++c.t, ++x) {
+      if (!(ok = wait_w(full(st), ph & 1))) break;
+      {
+        const uint32_t vb = ring0 + st * kStage, kb = vb + kOffK, ksb = vb + kOffKs, vsb = vb + kOffVs;
+        // ---- S = Q K^T, 8 keys at a time
+        float S[4][4];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          uint32_t kw[6], kh[6];
+          const uint32_t ka = kb + (8 * nb + r0) * kI4KCodes + 24 * q4;
+          const uint32_t sa = ksb + (8 * nb + 2 * q4) * 2 * kI4KGroups;  // keys 2 q4 and 2 q4 + 1
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            lds64(ka + 8 * i, kw[2 * i], kw[2 * i + 1]);
+            lds64(sa + 8 * i, kh[2 * i], kh[2 * i + 1]);
+          }
+          uint64_t s01 = 0, s23 = 0;
+#pragma unroll
+          for (int j = 0; j < kI4KGroups; ++j) {
+            const uint32_t wd = kw[j], w8 = wd >> 8;
+            const float c0[4] = {ck[j][0], ck[j][0], ck[j][1], ck[j][1]};
+            float d[4];
+            mma_f16_c(d, qa[2 * j], wd & kI4Lo, wd & kI4Hi, c0);
+            mma_f16_c(d, qa[2 * j + 1], w8 & kI4Lo, w8 & kI4Hi, d);
+            const float2 sA = f32x2_of_f16x2(kh[j >> 1]), sB = f32x2_of_f16x2(kh[3 + (j >> 1)]);
+            const uint64_t sc = (j & 1) ? pack_f32x2(sA.y, sB.y) : pack_f32x2(sA.x, sB.x);
+            s01 = fma_f32x2(pack_f32x2(d[0], d[1]), sc, s01);
+            s23 = fma_f32x2(pack_f32x2(d[2], d[3]), sc, s23);
+          }
+          S[nb][0] = lo_f32(s01);
+          S[nb][1] = hi_f32(s01);
+          S[nb][2] = lo_f32(s23);
+          S[nb][3] = hi_f32(s23);
+        }
+        // ---- value scales of keys 2 q4, 2 q4 + 1 of each 8: [group] fp16 pairs (even, odd key)
+        uint32_t vs[4][kI4VGroups];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          uint32_t h[4];
+          lds128(vsb + (8 * nb + 2 * q4) * 2 * kI4VGroups, h);
+          vs[nb][0] = __byte_perm(h[0], h[2], 0x5410);
+          vs[nb][1] = __byte_perm(h[0], h[2], 0x7632);
+          vs[nb][2] = __byte_perm(h[1], h[3], 0x5410);
+          vs[nb][3] = __byte_perm(h[1], h[3], 0x7632);
+        }
+        // ---- masks, only in tiles that some row does not see whole.  A slot nothing was written
+        // to may hold any scale: it counts as 0
+        const int key0 = (U.t0 + c.t) * kTile;
+        if (ring || key0 < lo_all || key0 + kTile - 1 > hi_all) {
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int col = 8 * nb + 2 * q4 + e;
+              int kp = key0 + col;
+              if (ring) {
+                const int j = kp + ring_off;
+                kp = kp < R ? ctx - R + (j >= R ? j - R : j) : -1;
+              }
+              if (!(kp >= 0 && kp < U.end))
+#pragma unroll
+                for (int u = 0; u < kI4VGroups; ++u) vs[nb][u] &= e ? 0x0000FFFFu : 0xFFFF0000u;
+              if (!(kp >= lo_r[0] && kp <= hi_r[0])) S[nb][e] = -INFINITY;
+              if (!(kp >= lo_r[1] && kp <= hi_r[1])) S[nb][2 + e] = -INFINITY;
+            }
+        }
+        // ---- running maximum and sum
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          mx[0] = fmaxf(mx[0], fmaxf(S[nb][0], S[nb][1]));
+          mx[1] = fmaxf(mx[1], fmaxf(S[nb][2], S[nb][3]));
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
+          mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
+          mx[hf] = fmaxf(m_r[hf], mx[hf] * c_log2);
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m_r[0] || mx[1] > m_r[1])) {
+          // (a row that has seen no key yet: its sums are zero, whatever the factor)
+          const float al0 = mx[0] == -INFINITY ? 1.f : ex2(m_r[0] - mx[0]);
+          const float al1 = mx[1] == -INFINITY ? 1.f : ex2(m_r[1] - mx[1]);
+          m_r[0] = mx[0];
+          m_r[1] = mx[1];
+          l_r[0] *= al0;
+          l_r[1] *= al1;
+#pragma unroll
+          for (int u = 0; u < kI4VGroups; ++u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[u][e][0] *= al0;
+              o[u][e][1] *= al0;
+              o[u][e][2] *= al1;
+              o[u][e][3] *= al1;
+            }
+            T[u][0] *= al0;
+            T[u][2] *= al1;
+          }
+        }
+        const float mu0 = m_r[0] == -INFINITY ? 0.f : m_r[0] - kPBias, mu1 = m_r[1] == -INFINITY ? 0.f : m_r[1] - kPBias;
+        uint32_t P[4][2];  // (p of the even key, -p of the odd key) of rows r0, r0 + 8
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          const float a0 = ex2(fmaf(S[nb][0], c_log2, -mu0)), a1 = ex2(fmaf(S[nb][1], c_log2, -mu0));
+          const float b0 = ex2(fmaf(S[nb][2], c_log2, -mu1)), b1 = ex2(fmaf(S[nb][3], c_log2, -mu1));
+          l_r[0] += a0 + a1;
+          l_r[1] += b0 + b1;
+          P[nb][0] = pack2_f16(a0, -a1);
+          P[nb][1] = pack2_f16(b0, -b1);
+        }
+        // ---- O += P V, 16 keys at a time
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const int row = 16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+          for (int up = 0; up < 2; ++up) {
+            uint32_t m[4];
+            ldsm_x4_t(vb + row * kI4VCodes + (((2 * up + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), m);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int u = 2 * up + h;
+              uint32_t pa[4];
+              pa[0] = hmul2(P[2 * kk][0], vs[2 * kk][u]);
+              pa[1] = hmul2(P[2 * kk][1], vs[2 * kk][u]);
+              pa[2] = hmul2(P[2 * kk + 1][0], vs[2 * kk + 1][u]);
+              pa[3] = hmul2(P[2 * kk + 1][1], vs[2 * kk + 1][u]);
+              const uint32_t x0 = m[2 * h], x1 = m[2 * h + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+              constexpr uint32_t cl = 0x000F0000u, ch = 0x00F00000u;  // the odd key's complement
+              mma_f16_c(o[u][0], pa, (x0 & kI4Lo) ^ cl, (x1 & kI4Lo) ^ cl, o[u][0]);
+              mma_f16_c(o[u][1], pa, (x0 & kI4Hi) ^ ch, (x1 & kI4Hi) ^ ch, o[u][1]);
+              mma_f16_c(o[u][2], pa, (y0 & kI4Lo) ^ cl, (y1 & kI4Lo) ^ cl, o[u][2]);
+              mma_f16_c(o[u][3], pa, (y0 & kI4Hi) ^ ch, (y1 & kI4Hi) ^ ch, o[u][3]);
+              // p (n - 8) = p n - 8 p for the even key, -p (15 - n) + 7 p for the odd one
+              mma_f16_c(T[u], pa, 0xC700C800u, 0xC700C800u, T[u]);
+            }
+          }
+        }
+      }
+      // ---- release the stage; the leader refills the one before it (other warps may still read this one)
+      __syncwarp();
+      if (nc > 1) {
+        if (lane == 0) mbar_arrive(empty(st));
+        if (leader && behind && !(ok = issue())) break;
+        behind = true;
+      } else if (!(ok = issue())) {
+        break;
+      }
+      if (++st == stages) st = 0, ++ph;
+    }
+    if (!ok) break;
+
+    // ---- the segment's rows
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      l_r[hf] += __shfl_xor_sync(0xffffffffu, l_r[hf], 1);
+      l_r[hf] += __shfl_xor_sync(0xffffffffu, l_r[hf], 2);
+    }
+    const bool direct = t_first == 0 && c.t == c.nt;
+    const long piece = 2L * w + (x - (c.t - t_first) > a ? 1 : 0);  // this worker's first or last segment
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      if (draft[hf] >= p.q_len) continue;
+      const int rr = blk * 16 + r0 + 8 * hf, h = g * G + rr % G;
+      const long qrow = long(s) * p.q_len + draft[hf];
+      const float M = m_r[hf] - kPBias, L = l_r[hf];
+      float M2 = M, L2 = L, sc = 1.f;
+      if (direct) {
+        float f = 1.f;
+        if (p.sink) {
+          const float sl = p.sink[h] * kLog2e;
+          M2 = fmaxf(M, sl);
+          f = ex2(M - M2);
+          L2 = L * f + ex2(sl - M2);
+        }
+        sc = p.v_scale * f / L2;
+        if (p.lse && q4 == 0) p.lse[qrow * kHq + h] = (M2 + __log2f(L2)) * kLn2;
+      } else if (q4 == 0) {
+        *reinterpret_cast<float2*>(p.ws_ml + (piece * rows + rr) * 2) = make_float2(M, L);
+      }
+#pragma unroll
+      for (int u = 0; u < kI4VGroups; ++u) {
+        float f[8];  // dims 32 u + 8 q4 + i
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          f[i] = fmaf(o[u][i & 3][2 * hf + (i >> 2)], (i & 1) ? 0x1p20f : 0x1p24f, T[u][2 * hf]) * sc;
+        if (direct) {
+          *reinterpret_cast<uint4*>(p.out + (qrow * kHq + h) * kDv + 32 * u + 8 * q4) =
+              make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + (piece * rows + rr) * kDv + 32 * u + 8 * q4);
+          dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+          dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+      }
+    }
+  }
+  if (!ok) drain();
+}
+
+// One warp per (query row, head): merges the pieces that share the row's unit, in their order.
+__global__ void __launch_bounds__(256) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
+  const int wid = int((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  if (wid >= p.batch * p.q_len * kHq) return;
+  const int qrow = wid / kHq, h = wid % kHq, s = qrow / p.q_len, g = h / p.group;
+  const long long total = p.ws_tbl[p.batch] * p.hkv;
+  const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
+  if (nt == 0) return;
+  const long long u0 = p.ws_tbl[s] * p.hkv + g * nt;
+  const int W = workers_of(p, total);
+  const int w0 = int(((u0 + 1) * W - 1) / total), w1 = int(((u0 + nt) * W - 1) / total);
+  if (w0 == w1) return;  // one piece holds the unit: its rows are written
+  const int rows = p.n_blocks * 16, rr = (qrow - s * p.q_len) * p.group + h % p.group;
+  // the first piece's unit is that piece's last segment, unless it begins with it
+  const long first = 2L * w0 + (u0 > w0 * total / W ? 1 : 0);
+  auto piece = [&](int i) { return (i == 0 ? first : 2L * (w0 + i)) * rows + rr; };
+  const int n = w1 - w0 + 1;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float sl = -INFINITY;
+  if (p.sink) {
+    sl = p.sink[h] * kLog2e;
+    M = fmaxf(M, sl);
+  }
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * piece(i));
+    const float f = ex2(ml.x - M);
+    const float4 v = *reinterpret_cast<const float4*>(p.ws_o + piece(i) * kDv + lane * 4);
+    L += f * ml.y;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+  if (p.sink) L += ex2(sl - M);
+  const float sc = p.v_scale / L;
+  *reinterpret_cast<uint2*>(p.out + (long(qrow) * kHq + h) * kDv + lane * 4) =
+      make_uint2(pack2_bf16(acc.x * sc, acc.y * sc), pack2_bf16(acc.z * sc, acc.w * sc));
+  if (p.lse && lane == 0) p.lse[long(qrow) * kHq + h] = (M + __log2f(L)) * kLn2;
+}
+
+Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms) {
+  Decode4Plan d;
+  d.n_blocks = (q_len * (kHq / hkv) + 15) / 16;
+  d.nc = d.n_blocks;
+  d.groups = kWarps / d.nc;
+  d.stages = kAllStages / d.groups;
+  const int tiles = (unit_keys + kTile - 1) / kTile + 1;  // a window may begin inside a tile
+  // A unit of up to 8 tiles stays whole: a second kernel would cost more than it saves.
+  d.whole_units = ring || tiles <= 9;
+  d.min_tiles = 4;
+  const long long units = (long long)batch * hkv;
+  const long long most = d.whole_units ? units : (units * tiles + d.min_tiles - 1) / d.min_tiles;
+  d.workers = int(most < (long long)sms * d.groups ? most : (long long)sms * d.groups);
+  return d;
+}
+
+cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end) {
+  cudaError_t e;
+  if (ev_begin && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_begin), s)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(decode4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  decode4_kernel<<<p.workers < sms ? p.workers : sms, kWarps * 32, kSmem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (ev_end && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_end), s)) != cudaSuccess) return e;
+  if (p.whole_units) return cudaSuccess;
+  const long warps = long(p.batch) * p.q_len * kHq;
+  decode4_combine_kernel<<<unsigned((warps * 32 + 255) / 256), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mimo

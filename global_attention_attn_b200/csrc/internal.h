@@ -25,6 +25,7 @@ struct AppendParams {
   const uint16_t* v_new;
   const int32_t* pos;
   const int32_t* seq_idx;
+  const int32_t* slots;      // cache slot of each token, or null (its position)
   int cache_kind;
   uint16_t* k_cache;
   uint16_t* v_cache;
@@ -33,6 +34,7 @@ struct AppendParams {
   const int32_t* block_table;
   int max_pages, num_pages;
   int fp8;                   // cache rows hold E4M3 bytes (quantised by 1 / k_dequant[g], 1 / v_dequant[g])
+  int int4;                  // cache blocks hold 4-bit codes and group scales (int4.cuh)
   const float* k_dequant;
   const float* v_dequant;
   RopeFreqs rope;
@@ -53,6 +55,7 @@ struct DecodeParams {
   const float* sink;
   const uint16_t* q;
   const int32_t* seq_lens;
+  const int32_t* positions;  // rotary position of each sequence's last query token, or null (seq_lens - 1)
   int cache_kind;
   int ring_slots;  // ring: slots per sequence (a multiple of the 16-key tile)
   const uint16_t* k_cache;
@@ -68,6 +71,39 @@ struct DecodeParams {
   const float* v_dequant;
   RopeFreqs rope;
   unsigned* status;
+};
+
+// Decode over a 4-bit cache (decode_int4.cu).
+constexpr int kI4Tile = 32;        // keys per tile
+constexpr int kI4MaxBatch = 1024;  // sequences per launch (a prefix table in shared memory)
+struct Decode4Params {
+  CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, 32, 1}
+  int batch, hkv, group, q_len, n_blocks;
+  int nc, groups, stages;      // warps per worker (one per row block), workers per CTA, stages per worker
+  int workers, min_tiles;      // workers at most; tiles a worker takes at least
+  int whole_units;             // pieces hold whole (sequence, KV head) units: no combine
+  int window, max_seq_len;
+  float scale_log2, v_scale;
+  const float* sink;
+  const uint16_t* q;
+  const int32_t* seq_lens;
+  const int32_t* positions;
+  int cache_kind, ring_slots;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* block_table;
+  int max_pages, num_pages;
+  long block0;  // ring: block of the launch's first sequence
+  uint16_t* out;
+  float* lse;
+  float* ws_o;        // [2 * workers, 16 * n_blocks, 128]: a worker's first and last segment
+  float* ws_ml;       // [2 * workers, 16 * n_blocks, 2]
+  long long* ws_tbl;  // [batch + 1] tiles per KV head before each sequence, for the combine
+  RopeFreqs rope;
+  unsigned* status;
+};
+struct Decode4Plan {
+  int n_blocks, nc, groups, stages, workers, min_tiles, whole_units;
 };
 
 // Key source modes of the prefill kernel.
@@ -149,6 +185,9 @@ cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t s);
 // Row blocks of a decode unit (q_len rows of `group` heads), consumer warps per producer and
 // row parts per unit.
 void decode_rows(int q_len, int group, int* n_blocks, int* nc, int* n_rp);
+// unit_keys: keys a (sequence, KV head) covers at most
+Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms);
+cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end);
 cudaError_t launch_rope_k(const RopeKParams& p, cudaStream_t s);
 // kind 0: sliding window (G=8 heads x 16 rows, one 144-key tile); kind 1: global (G=16 x 8 rows, 128-key tiles)
 // pdl: launch with programmatic stream serialization (the kernel's prologue overlaps the key

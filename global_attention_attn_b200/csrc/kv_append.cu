@@ -2,16 +2,38 @@
 // store key and value into the ring or paged cache.  Cache rows hold the key
 // as dims 0..63 rotated in IEEE fp16 and dims 64..191 in bf16 (the input
 // format), and the value in bf16; or, for an E4M3 cache, every element as one
-// E4M3 byte scaled by 1 / (its KV head's dequantisation scale).
+// E4M3 byte scaled by 1 / (its KV head's dequantisation scale); or, for a 4-bit cache, codes
+// with a scale per 32 dims.
 //
 // Cache layout follows the serving pages: window-sized KV for the sliding
 // layers (gaudi-cookbook "MiMo-V2.6-Flash-RL", "Launch": window-sized KV for
 // the 39 sliding layers) kept here as a 128-slot ring per sequence, and paged
 // KV with block size 128 for the global layers (same page, "--block-size 128").
 #include "common.cuh"
+#include "int4.cuh"
 #include "../../include/mimoattn.h"
 
 namespace mimo {
+
+namespace {
+// The cache entry (slot of the whole pool, in units of one KV row set) of token t; -1 and a
+// status bit if its sequence, position, slot or page lies outside the cache.
+__device__ __forceinline__ long append_entry(const AppendParams& p, int t, int pos, int lane) {
+  const int s = p.seq_idx[t], at = p.slots ? p.slots[t] : pos;
+  bool ok = s >= 0 && s < p.num_seqs && pos >= 0 && at >= 0;
+  long entry = -1;
+  if (ok && p.cache_kind == MIMO_CACHE_RING) {
+    entry = long(s) * p.ring_slots + (at % p.ring_slots);
+  } else if (ok) {
+    const int pi = at / kPage;
+    const int page = pi < p.max_pages ? p.block_table[long(s) * p.max_pages + pi] : -1;
+    ok = page >= 0 && page < p.num_pages;
+    if (ok) entry = long(page) * kPage + (at % kPage);
+  }
+  if (!ok && lane == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+  return entry;
+}
+}  // namespace
 
 // One warp per (token, kv head).  Lanes 0..3 rotate the chunk pairs (u, u+4) of
 // dims 0..63; lanes 8..23 copy chunks 8..23 (dims 64..191); lanes 0..15 copy V.
@@ -20,23 +42,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   const int lane = threadIdx.x & 31;
   if (warp >= p.num_tokens * p.hkv) return;
   const int t = warp / p.hkv, g = warp % p.hkv;
-  const int pos = p.pos[t], s = p.seq_idx[t];
-  long entry;
-  if (s < 0 || s >= p.num_seqs || pos < 0) {
-    if (lane == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-    return;
-  }
-  if (p.cache_kind == MIMO_CACHE_RING) {
-    entry = long(s) * p.ring_slots + (pos % p.ring_slots);
-  } else {
-    const int pi = pos / kPage;
-    const int page = pi < p.max_pages ? p.block_table[long(s) * p.max_pages + pi] : -1;
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-      return;
-    }
-    entry = long(page) * kPage + (pos % kPage);
-  }
+  const int pos = p.pos[t];
+  const long entry = append_entry(p, t, pos, lane);
+  if (entry < 0) return;
   const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + (long(t) * p.hkv + g) * kDqk);
   if (p.fp8) {
     // E4M3 rows: each element divided by its KV head's dequantisation scale, rounded to
@@ -106,12 +114,94 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   }
 }
 
+// 4-bit rows (int4.cuh): one warp per (token, KV head), bound by its 640 bytes read and 180
+// written.  Lane l holds key dims 8 l .. 8 l + 7 (l < 24) and value dims 8 l .. (l < 16), so a
+// group of 32 dims is four neighbouring lanes, its largest magnitude two shuffles, and a
+// lane's codes one word.  Per group: scale = fp16(amax / 7), code = rint(x / scale) + 8 with
+// x / scale the fp32 quotient; 7 of amax keeps zero exact and both signs alike.
+__global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams p) {
+  const int warp = int((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+  const int lane = threadIdx.x & 31;
+  if (warp >= p.num_tokens * p.hkv) return;
+  const int t = warp / p.hkv, g = warp % p.hkv;
+  const int pos = p.pos[t];
+  const long entry = append_entry(p, t, pos, lane);
+  if (entry < 0) return;
+  const int slots = p.cache_kind == MIMO_CACHE_RING ? p.ring_slots : kPage;
+  const long block = entry / slots * p.hkv + g;
+  const int slot = int(entry % slots);
+  uint8_t* kb = reinterpret_cast<uint8_t*>(p.k_cache) + block * (long(slots) * kI4KSlot);
+  uint8_t* vb = reinterpret_cast<uint8_t*>(p.v_cache) + block * (long(slots) * kI4VSlot);
+  const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + (long(t) * p.hkv + g) * kDqk);
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + (long(t) * p.hkv + g) * kDv);
+  const uint4 kr = lane < 24 ? __ldg(ks + lane) : make_uint4(0, 0, 0, 0);
+  const uint4 vr = lane < 16 ? __ldg(vs + lane) : make_uint4(0, 0, 0, 0);
+  auto widen = [](const uint4& c, float* x) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = lo_bf16(w[i]);
+      x[2 * i + 1] = hi_bf16(w[i]);
+    }
+  };
+  // 8 dims of a group -> their word of codes; every lane of the warp takes part
+  auto quantise = [&](const float* x, float cap, float& scale, bool& range) -> uint32_t {
+    float amax = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      amax = fmaxf(amax, fabsf(x[i]));
+      bad = bad || !(fabsf(x[i]) < INFINITY);
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float want = __fdiv_rn(amax, 7.f);
+    scale = __half2float(__float2half_rn(fminf(want, cap)));
+    range = range || bad || want > cap;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float n = scale > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -7.f), 7.f) : 0.f;
+      w |= uint32_t(int(n) + 8) << (4 * i);
+    }
+    return w;
+  };
+  bool range = false;
+  float x[8], scale;
+  widen(kr, x);
+  float c, sn;
+  rope_cos_sin(pos, p.rope.inv_freq[lane], &c, &sn);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // lanes 0..3 hold dims 8 l + i, lanes 4..7 their partners + 32
+    const float ci = __shfl_sync(0xffffffffu, c, 8 * (lane & 3) + i), si = __shfl_sync(0xffffffffu, sn, 8 * (lane & 3) + i);
+    const float y = __shfl_xor_sync(0xffffffffu, x[i], 4);
+    if (lane < 4) x[i] = x[i] * ci - y * si;
+    else if (lane < 8) x[i] = x[i] * ci + y * si;
+  }
+  const uint32_t kw = quantise(x, kF16Max, scale, range);
+  if (lane < 24) {
+    reinterpret_cast<uint32_t*>(kb + long(slot) * kI4KCodes)[(lane & 3) * 6 + (lane >> 2)] = kw;
+    if ((lane & 3) == 0)
+      reinterpret_cast<__half*>(kb + long(slots) * kI4KCodes)[slot * kI4KGroups + (lane >> 2)] = __float2half_rn(scale);
+  }
+  widen(vr, x);
+  const uint32_t vw = quantise(x, kI4VScaleMax, scale, range);
+  if (lane < 16) {
+    reinterpret_cast<uint32_t*>(vb + long(slot) * kI4VCodes)[lane] = vw;
+    if ((lane & 3) == 0)
+      reinterpret_cast<__half*>(vb + long(slots) * kI4VCodes)[slot * kI4VGroups + (lane >> 2)] = __float2half_rn(scale);
+  }
+  if (range) atomicOr(p.status, MIMO_STATUS_RANGE);
+}
+
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s) {
   const long warps = long(p.num_tokens) * p.hkv;
   if (warps == 0) return cudaSuccess;
   const int block = 256;
   const long grid = (warps * 32 + block - 1) / block;
-  kv_append_kernel<<<unsigned(grid), block, 0, s>>>(p);
+  if (p.int4) kv_append_int4_kernel<<<unsigned(grid), block, 0, s>>>(p);
+  else kv_append_kernel<<<unsigned(grid), block, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -58,7 +58,9 @@ extern "C" {
 #define MIMO_STATUS_TIMEOUT 1u    /* a bounded barrier / copy wait ran out */
 #define MIMO_STATUS_BAD_INDEX 2u  /* a page id, slot or position outside its cache */
 #define MIMO_STATUS_RANGE 4u      /* a rotated query / key component beyond fp16's range,
-                                     stored saturated at +-65504 */
+                                     stored saturated at +-65504; 4-bit caches: a query
+                                     component beyond +-16376, a group scale beyond its range,
+                                     an element that is not finite */
 #define MIMO_STATUS_BAD_SCALE 8u  /* an E4M3 dequantisation scale not finite and positive */
 
 /* The attention layer.  num_q_heads 64, head_dim_qk 192, head_dim_v 128 and
@@ -121,9 +123,25 @@ MIMO_API int mimo_window_from_left_right(int left, int right, int* window);
  *     recipe page for MiMo-V2.6-Flash ("Launch command", the AMD MI355X line)
  *     serves the model with an FP8 KV cache (--kv-cache-dtype fp8) without
  *     saying how it is scaled; one scale per KV head is this library's reading.
- *     It halves the bytes a decode step streams. */
+ *     It halves the bytes a decode step streams.
+ *   MIMO_DTYPE_INT4: every element is a 4-bit code that stands for (code - 8) * scale, with
+ *     one fp16 scale per 32 consecutive dims of a slot (6 of a key, 4 of a value), stored with
+ *     the codes (k_dequant / v_dequant are NULL): 180 bytes per slot and KV head against 640
+ *     (bf16).  Appends and decode (any q_len, ring and paged); prefill reads bf16 caches.
+ *     The KV head is outside the slot here: k_cache is [num_pages or num_seqs, Hkv, S * 108]
+ *     bytes and v_cache [.., Hkv, S * 72] (S = 128 or ring_slots): a head's S rows of codes (96
+ *     and 64 bytes), then its S rows of scales (6 and 4 fp16).  Byte i of a row of codes holds
+ *     dims 2i (low four bits) and 2i + 1; a key row's 24 words of 8 dims are stored as word w
+ *     at (w % 4) * 6 + w / 4.  An append stores scale = fp16(amax / 7) of the group's largest
+ *     magnitude amax (fp32 quotient) and code = 8 + rint(x / scale), -7 <= code - 8 <= 7; a
+ *     scale beyond 65504 (keys) or 1023 (values) is stored as that limit, an element that is
+ *     not finite as +-7 (MIMO_STATUS_RANGE).  Codes and scales made elsewhere are read as
+ *     they are (code 0 too); value scales must not pass 1023 in magnitude. */
 #define MIMO_DTYPE_BF16 0
 #define MIMO_DTYPE_FP8_E4M3 1
+#define MIMO_DTYPE_INT4 2
+#define MIMO_INT4_K_SLOT_BYTES 108
+#define MIMO_INT4_V_SLOT_BYTES 72
 
 /*
  * Prefill (varlen, causal, window or global, sink on/off).
@@ -227,7 +245,16 @@ MIMO_API int mimo_attn_prefill_stall_test(const mimo_prefill_args* args, void* s
  * split-KV decode kernel; draft rows (q_len >= 2) of a global layer (4 KV heads, no
  * window) on a bf16 paged cache run the tensor-core prefill kernel, whose 128-row tile
  * holds the q_len x 16 query rows of one KV head, over page-aligned splits, then the same
- * combine pass.  Either way the split-KV workspace is the one the size queries give.
+ * combine pass.  Either way the split-KV workspace is the one the size queries give.  4-bit
+ * caches (MIMO_DTYPE_INT4) have a decode kernel and a workspace size query of their own
+ * (mimo_attn_decode_int4_workspace_size); there a seq_lens above max_seq_len is always
+ * reported, and its keys from max_seq_len on are not attended.
+ *
+ * positions (device int32 [batch], or NULL): the rotary position of each sequence's last
+ * query token, where it is not seq_lens[s] - 1: after an eviction the cache holds fewer
+ * slots than the sequence has tokens, and the keys carry the positions they were appended
+ * with.  seq_lens then counts slots, and query row i sees slots 0 .. seq_lens[s] - q_len + i.
+ * Paged caches without a window only (MIMO_ERR_INVALID_ARG otherwise).
  */
 #define MIMO_MAX_DRAFTS 8
 typedef struct {
@@ -252,11 +279,12 @@ typedef struct {
    * cudaEventElapsedTime gives that kernel's device time. */
   void* ev_kernel_begin;
   void* ev_kernel_end;
-  int cache_dtype;          /* MIMO_DTYPE_BF16 (default 0) or MIMO_DTYPE_FP8_E4M3 */
+  int cache_dtype;          /* MIMO_DTYPE_BF16 (default 0), MIMO_DTYPE_FP8_E4M3 or MIMO_DTYPE_INT4 */
   const float* k_dequant;   /* FP8: device fp32 [num_kv_heads] key scales, else NULL */
   const float* v_dequant;   /* FP8: device fp32 [num_kv_heads] value scales, else NULL */
   int ring_slots;           /* MIMO_CACHE_RING: slots per sequence of the ring (0 = 128) */
   int q_len;                /* query tokens per sequence: 0 or 1 (decode), up to MIMO_MAX_DRAFTS */
+  const int32_t* positions; /* device int32 [batch] rotary positions, or NULL (seq_lens - 1) */
 } mimo_decode_args;
 
 /* Bytes of workspace mimo_attn_decode needs (split-KV partials) for one query token per
@@ -266,6 +294,11 @@ MIMO_API size_t mimo_attn_decode_workspace_size(int batch, int max_seq_len, int 
 /* The same for q_len query tokens per sequence (0 for q_len outside 1..MIMO_MAX_DRAFTS). */
 MIMO_API size_t mimo_attn_verify_workspace_size(int batch, int q_len, int max_seq_len, int num_kv_heads,
                                                 int window);
+
+/* The same for a 4-bit cache (MIMO_DTYPE_INT4) of the given kind; at most 20 MB, whatever the
+ * batch.  0 for sizes that a call refuses. */
+MIMO_API size_t mimo_attn_decode_int4_workspace_size(int batch, int q_len, int max_seq_len, int num_kv_heads,
+                                                     int window, int cache_kind);
 
 MIMO_API int mimo_attn_decode(const mimo_decode_args* args, void* stream);
 
@@ -287,7 +320,8 @@ MIMO_API int mimo_attn_decode(const mimo_decode_args* args, void* stream);
  *     device's context has changed since (after a device reset).
  *   - Problems whose partials need more than MIMO_DECODE_NOALLOC_MAX_BYTES
  *     (mimo_attn_decode_workspace_size of the same sizes) are rejected with
- *     MIMO_ERR_WORKSPACE before anything is enqueued.
+ *     MIMO_ERR_WORKSPACE before anything is enqueued.  (4-bit caches are never rejected: their
+ *     work is cut into as many pieces as the array has room for.)
  *   - All calls share the one array, so calls whose kernels overlap on the GPU
  *     (different streams, or different host threads) race and corrupt each
  *     other's results; serialise them.  No part of the array needs to start at
@@ -310,6 +344,10 @@ MIMO_API int mimo_attn_decode_noalloc(const mimo_decode_args* args, void* stream
  * finite and positive; a token of a KV head whose scale is not is skipped and sets
  * MIMO_STATUS_BAD_SCALE.  A rotated key component beyond the fp16 range (|x| > 65504)
  * is stored as +-65504 and sets MIMO_STATUS_RANGE (bf16 caches).
+ *
+ * slots (device int32 [num_tokens], or NULL): the slot each token is stored in, counted within
+ * its sequence, where it is not pos[t] (an evicted cache: the rotation takes pos[t], the
+ * page and slot come from slots[t]).  Paged caches only.
  */
 typedef struct {
   int num_tokens;
@@ -329,10 +367,11 @@ typedef struct {
   const int32_t* block_table; /* paged: device int32 [num_seqs, max_pages] */
   int max_pages;
   int num_pages;
-  int cache_dtype;          /* MIMO_DTYPE_BF16 (default 0) or MIMO_DTYPE_FP8_E4M3 */
+  int cache_dtype;          /* MIMO_DTYPE_BF16 (default 0), MIMO_DTYPE_FP8_E4M3 or MIMO_DTYPE_INT4 */
   const float* k_dequant;   /* FP8: device fp32 [num_kv_heads], else NULL */
   const float* v_dequant;
   int ring_slots;           /* MIMO_CACHE_RING: slots per sequence of the ring (0 = 128) */
+  const int32_t* slots;     /* device int32 [num_tokens], or NULL (the slot of pos) */
 } mimo_append_args;
 
 MIMO_API int mimo_kv_append(const mimo_append_args* args, void* stream);
