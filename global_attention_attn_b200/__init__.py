@@ -32,6 +32,7 @@ MIMO_DTYPE_FP8_E4M3 = 1
 MIMO_DTYPE_INT4 = 2
 MIMO_INT4_K_SLOT_BYTES = 108
 MIMO_INT4_V_SLOT_BYTES = 72
+MIMO_SELECT_MAX_SLOTS = 393216
 MIMO_RING_SLOTS_DEFAULT = 128
 MIMO_RING_SLOTS_MAX = 512
 MIMO_MAX_DRAFTS = 8
@@ -46,7 +47,7 @@ V_SCALE = 0.707
 EXPORTS = ("mimo_attn_prefill", "mimo_attn_prefill_workspace_size", "mimo_attn_prefill_stall_test", "mimo_attn_decode",
            "mimo_attn_decode_workspace_size", "mimo_attn_verify_workspace_size",
            "mimo_attn_decode_int4_workspace_size", "mimo_attn_decode_noalloc",
-           "mimo_kv_append", "mimo_last_error",
+           "mimo_kv_append", "mimo_attn_weights", "mimo_kv_select", "mimo_kv_gather", "mimo_last_error",
            "mimo_status_poll", "mimo_version", "mimo_window_from_left_right")
 DECODE_NOALLOC_MAX_BYTES = 16 << 20
 
@@ -87,6 +88,27 @@ class MimoAppendArgs(C.Structure):
                 ("ring_slots", C.c_int), ("slots", _P)]
 
 
+class MimoWeightsArgs(C.Structure):
+    _fields_ = [("layer", MimoLayer), ("batch", C.c_int), ("q_len", C.c_int), ("max_seq_len", C.c_int), ("q", _P),
+                ("lse", _P), ("seq_lens", _P), ("positions", _P), ("k_cache", _P), ("block_table", _P),
+                ("max_pages", C.c_int), ("num_pages", C.c_int), ("cache_dtype", C.c_int), ("k_dequant", _P),
+                ("scores", _P), ("score_stride", C.c_int)]
+
+
+class MimoSelectArgs(C.Structure):
+    _fields_ = [("num_seqs", C.c_int), ("num_kv_heads", C.c_int), ("scores", _P), ("score_stride", C.c_int),
+                ("seq_lens", _P), ("max_seq_len", C.c_int), ("keep", C.c_int), ("recent", C.c_int), ("first", C.c_int),
+                ("idx", _P), ("counts", _P), ("scores_out", _P)]
+
+
+class MimoGatherArgs(C.Structure):
+    _fields_ = [("num_seqs", C.c_int), ("num_kv_heads", C.c_int), ("k_src", _P), ("v_src", _P),
+                ("block_table_src", _P), ("max_pages_src", C.c_int), ("num_pages_src", C.c_int), ("k_dst", _P),
+                ("v_dst", _P), ("block_table_dst", _P), ("max_pages_dst", C.c_int), ("num_pages_dst", C.c_int),
+                ("counts", _P), ("idx", _P), ("idx_stride", C.c_int), ("max_count", C.c_int),
+                ("cache_dtype", C.c_int), ("out_dtype", C.c_int), ("k_dequant", _P), ("v_dequant", _P)]
+
+
 _lib = None
 
 
@@ -122,6 +144,12 @@ def lib():
         L.mimo_attn_decode_noalloc.restype = C.c_int
         L.mimo_kv_append.argtypes = [C.POINTER(MimoAppendArgs), _P]
         L.mimo_kv_append.restype = C.c_int
+        L.mimo_attn_weights.argtypes = [C.POINTER(MimoWeightsArgs), _P]
+        L.mimo_attn_weights.restype = C.c_int
+        L.mimo_kv_select.argtypes = [C.POINTER(MimoSelectArgs), _P]
+        L.mimo_kv_select.restype = C.c_int
+        L.mimo_kv_gather.argtypes = [C.POINTER(MimoGatherArgs), _P]
+        L.mimo_kv_gather.restype = C.c_int
         L.mimo_last_error.argtypes = []
         L.mimo_last_error.restype = C.c_char_p
         L.mimo_status_poll.argtypes = [C.POINTER(C.c_uint32)]
@@ -312,6 +340,82 @@ def mimo_kv_append(k_new, v_new, pos, seq_idx, *, rope_base: float, cache_kind: 
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
     a.ring_slots, a.slots = int(ring_slots), _ptr(slots)
     _check(lib().mimo_kv_append(C.byref(a), _stream(stream)))
+
+
+def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_base: float, k_cache,
+                      block_table, num_pages: int, cache_dtype: int = MIMO_DTYPE_BF16, k_dequant=None, positions=None,
+                      q_len: int = 1, softmax_scale: float = SOFTMAX_SCALE, stream=None):
+    """Adds the attention weights of a decode call (its q, lse, seq_lens, positions) to the float32
+    scores [batch, num_kv_heads, slots] of a paged cache's slots (see include/mimoattn.h).
+    Returns scores."""
+    if q.shape[0] % q_len:
+        raise ValueError("q holds batch * q_len rows")
+    B = q.shape[0] // q_len
+    if scores.ndim != 3 or scores.shape[0] != B or scores.shape[1] != num_kv_heads or not scores.is_contiguous():
+        raise ValueError("scores is a contiguous [batch, num_kv_heads, slots] tensor")
+    a = MimoWeightsArgs()
+    a.layer = make_layer(num_kv_heads, rope_base, 0, None, softmax_scale, 1.0)
+    a.batch, a.q_len, a.max_seq_len = B, int(q_len), int(max_seq_len)
+    a.q, a.lse, a.seq_lens, a.positions = _ptr(q), _ptr(lse), _ptr(seq_lens), _ptr(positions)
+    a.k_cache, a.block_table = _ptr(k_cache), _ptr(block_table)
+    a.max_pages, a.num_pages = block_table.shape[1], num_pages
+    a.cache_dtype, a.k_dequant = cache_dtype, _ptr(k_dequant)
+    a.scores, a.score_stride = _ptr(scores), scores.shape[2]
+    _check(lib().mimo_attn_weights(C.byref(a), _stream(stream)))
+    return scores
+
+
+def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int = 0, first: int = 0, idx=None,
+                   counts=None, scores_out=None, stream=None):
+    """The slots that stay of every (sequence, KV head): the first `first`, the last `recent`, and the
+    largest scores of the others, `keep` in all (see include/mimoattn.h).  scores: float32
+    [num_seqs, num_kv_heads, slots].  Returns (idx int32 [num_seqs, num_kv_heads, keep] ascending,
+    padded with -1; counts int32 [num_seqs]; the kept slots' scores, padded with 0)."""
+    import torch
+    if scores.ndim != 3 or not scores.is_contiguous():
+        raise ValueError("scores is a contiguous [num_seqs, num_kv_heads, slots] tensor")
+    n, h, slots = scores.shape
+    if idx is None:
+        idx = torch.empty((n, h, keep), dtype=torch.int32, device=scores.device)
+    if counts is None:
+        counts = torch.empty(n, dtype=torch.int32, device=scores.device)
+    if scores_out is None:
+        scores_out = torch.empty((n, h, keep), dtype=torch.float32, device=scores.device)
+    a = MimoSelectArgs()
+    a.num_seqs, a.num_kv_heads, a.scores, a.score_stride = n, h, _ptr(scores), slots
+    a.seq_lens, a.max_seq_len = _ptr(seq_lens), int(max_seq_len)
+    a.keep, a.recent, a.first = int(keep), int(recent), int(first)
+    a.idx, a.counts, a.scores_out = _ptr(idx), _ptr(counts), _ptr(scores_out)
+    _check(lib().mimo_kv_select(C.byref(a), _stream(stream)))
+    return idx, counts, scores_out
+
+
+def mimo_kv_gather(k_src, v_src, block_table_src, k_dst, v_dst, block_table_dst, counts, *, num_kv_heads: int,
+                   num_pages: int, num_pages_out: int, idx=None, max_count: int | None = None,
+                   cache_dtype: int = MIMO_DTYPE_BF16, out_dtype: int | None = None, k_dequant=None, v_dequant=None,
+                   stream=None):
+    """Moves slots idx[s, g, j] (None: slot j) of a paged cache to slots j < counts[s] of other pages
+    (see include/mimoattn.h).  out_dtype: cache_dtype (None), or MIMO_DTYPE_BF16 to widen an E4M3 or
+    4-bit cache.  max_count: upper bound of counts (None: what idx or the destination table holds)."""
+    a = MimoGatherArgs()
+    a.num_seqs, a.num_kv_heads = block_table_src.shape[0], num_kv_heads
+    if block_table_dst.shape[0] != a.num_seqs or counts.shape[0] != a.num_seqs:
+        raise ValueError("both block tables and counts have a row per sequence")
+    if idx is not None and (idx.ndim != 3 or tuple(idx.shape[:2]) != (a.num_seqs, num_kv_heads) or not idx.is_contiguous()):
+        raise ValueError("idx is a contiguous [num_seqs, num_kv_heads, n] tensor")
+    if max_count is None:
+        max_count = block_table_dst.shape[1] * 128
+        if idx is not None:
+            max_count = min(max_count, idx.shape[2])
+    a.k_src, a.v_src, a.block_table_src = _ptr(k_src), _ptr(v_src), _ptr(block_table_src)
+    a.max_pages_src, a.num_pages_src = block_table_src.shape[1], num_pages
+    a.k_dst, a.v_dst, a.block_table_dst = _ptr(k_dst), _ptr(v_dst), _ptr(block_table_dst)
+    a.max_pages_dst, a.num_pages_dst = block_table_dst.shape[1], num_pages_out
+    a.counts, a.idx, a.idx_stride = _ptr(counts), _ptr(idx), 0 if idx is None else idx.shape[2]
+    a.max_count = int(max_count)
+    a.cache_dtype, a.out_dtype = cache_dtype, cache_dtype if out_dtype is None else out_dtype
+    a.k_dequant, a.v_dequant = _ptr(k_dequant), _ptr(v_dequant)
+    _check(lib().mimo_kv_gather(C.byref(a), _stream(stream)))
 
 
 def empty_int4_cache(blocks: int, num_kv_heads: int, ring_slots: int = 0, device="cuda"):

@@ -249,6 +249,8 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
                                   ring ? ring_slots : decode_unit_keys(a->max_seq_len, a->layer.window, q_len), ring,
                                   d.sms < kI4Sms ? d.sms : kI4Sms);
   while (plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
+  if (!ring && (long(a->num_pages) * hkv > INT_MAX || long(a->max_seq_len) * a->batch / kI4Tile * hkv / plan.workers > INT_MAX / 2))
+    return fail(MIMO_ERR_UNSUPPORTED, "%s: num_pages * num_kv_heads, or the keys of one worker, pass 2^31", fn);
   {
     const cuuint64_t slots = ring ? ring_slots : kPage;
     const cuuint64_t blocks = cuuint64_t(ring ? a->batch : a->num_pages) * hkv;
@@ -866,6 +868,171 @@ int mimo_attn_decode_noalloc(const mimo_decode_args* a, void* stream) {
     b.workspace_bytes = MIMO_DECODE_NOALLOC_MAX_BYTES;
   }
   return decode_impl("mimo_attn_decode", &b, stream, true);
+}
+
+int mimo_attn_weights(const mimo_weights_args* a, void* stream) {
+  const char* fn = "mimo_attn_weights";
+  if (!a) return fail(MIMO_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  if (int rc = check_layer(fn, a->layer)) return rc;
+  if (a->layer.window != 0) return fail(MIMO_ERR_INVALID_ARG, "%s: window must be 0 (global layers)", fn);
+  if (a->batch < 0) return fail(MIMO_ERR_INVALID_ARG, "%s: batch must be >= 0", fn);
+  if (a->batch == 0) return MIMO_OK;
+  const int q_len = a->q_len == 0 ? 1 : a->q_len;
+  if (q_len < 1 || q_len > MIMO_MAX_DRAFTS)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: q_len must be 0..%d (got %d)", fn, MIMO_MAX_DRAFTS, a->q_len);
+  if (a->max_seq_len < q_len) return fail(MIMO_ERR_INVALID_ARG, "%s: max_seq_len is below q_len", fn);
+  if (a->score_stride < a->max_seq_len)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: score_stride is below max_seq_len", fn);
+  REQUIRE_PTR(a->q, "q");
+  REQUIRE_PTR(a->lse, "lse");
+  REQUIRE_PTR(a->seq_lens, "seq_lens");
+  REQUIRE_PTR(a->k_cache, "k_cache");
+  REQUIRE_PTR(a->block_table, "block_table");
+  REQUIRE_PTR(a->scores, "scores");
+  if (a->positions) REQUIRE_PTR(a->positions, "positions");
+  if (a->max_pages <= 0 || a->num_pages <= 0)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: max_pages and num_pages must be > 0", fn);
+  if (long(a->max_pages) * kPage < a->max_seq_len)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: max_pages * 128 is below max_seq_len", fn);
+  if (int rc = check_cache_dtype(fn, a->cache_dtype, a->k_dequant, a->cache_dtype == MIMO_DTYPE_FP8_E4M3 ? a->k_dequant : nullptr))
+    return rc;
+  const int hkv = a->layer.num_kv_heads;
+  if (long(a->num_pages) * kPage > INT_MAX) return fail(MIMO_ERR_UNSUPPORTED, "%s: num_pages * 128 passes 2^31", fn);
+  DevState d;
+  if (int rc = dev_state(fn, &d)) return rc;
+  WeightsParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (a->cache_dtype != MIMO_DTYPE_INT4) {
+    EncodeTiledFn enc;
+    if (int rc = get_encoder(fn, &enc)) return rc;
+    if (int rc = make_map(fn, enc, &p.tm_k, a->k_cache, long(a->num_pages) * kPage, hkv, kDqk, 1, 32,
+                          a->cache_dtype == MIMO_DTYPE_FP8_E4M3))
+      return rc;
+  }
+  p.hkv = hkv;
+  p.q_len = q_len;
+  p.max_seq_len = a->max_seq_len;
+  p.scale_log2 = a->layer.softmax_scale * 1.4426950408889634f;
+  p.k_cache = static_cast<const uint8_t*>(a->k_cache);
+  p.max_pages = a->max_pages;
+  p.num_pages = a->num_pages;
+  p.cache_dtype = a->cache_dtype;
+  p.k_dequant = a->k_dequant;
+  p.score_stride = a->score_stride;
+  p.rope = make_freqs(a->layer.rope_base);
+  p.status = d.status;
+  for (int s0 = 0; s0 < a->batch; s0 += kI4MaxBatch) {
+    p.batch = a->batch - s0 < kI4MaxBatch ? a->batch - s0 : kI4MaxBatch;
+    p.q = static_cast<const uint16_t*>(a->q) + long(s0) * q_len * kHq * kDqk;
+    p.lse = a->lse + long(s0) * q_len * kHq;
+    p.seq_lens = a->seq_lens + s0;
+    p.positions = a->positions ? a->positions + s0 : nullptr;
+    p.block_table = a->block_table + long(s0) * a->max_pages;
+    p.scores = a->scores + long(s0) * hkv * a->score_stride;
+    cudaError_t e = launch_weights(p, d.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  }
+  return MIMO_OK;
+}
+
+int mimo_kv_select(const mimo_select_args* a, void* stream) {
+  const char* fn = "mimo_kv_select";
+  if (!a) return fail(MIMO_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  if (a->num_kv_heads != 8 && a->num_kv_heads != 4)
+    return fail(MIMO_ERR_UNSUPPORTED, "%s: num_kv_heads must be 8 or 4", fn);
+  if (a->num_seqs < 0) return fail(MIMO_ERR_INVALID_ARG, "%s: num_seqs must be >= 0", fn);
+  if (a->max_seq_len <= 0 || a->max_seq_len > MIMO_SELECT_MAX_SLOTS)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: max_seq_len must be in 1..%d", fn, MIMO_SELECT_MAX_SLOTS);
+  if (a->score_stride < a->max_seq_len)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: score_stride is below max_seq_len", fn);
+  if (a->keep <= 0 || a->recent < 0 || a->first < 0 || long(a->recent) + a->first > a->keep)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: keep must be > 0, and recent and first >= 0 with recent + first <= keep", fn);
+  if (long(a->num_seqs) * a->num_kv_heads * 8 > INT_MAX)
+    return fail(MIMO_ERR_UNSUPPORTED, "%s: num_seqs is too large", fn);
+  if (a->num_seqs == 0) return MIMO_OK;
+  REQUIRE_PTR(a->scores, "scores");
+  REQUIRE_PTR(a->seq_lens, "seq_lens");
+  REQUIRE_PTR(a->idx, "idx");
+  REQUIRE_PTR(a->counts, "counts");
+  if (a->scores_out) REQUIRE_PTR(a->scores_out, "scores_out");
+  DevState d;
+  if (int rc = dev_state(fn, &d)) return rc;
+  SelectParams p;
+  p.num_seqs = a->num_seqs;
+  p.hkv = a->num_kv_heads;
+  p.scores = a->scores;
+  p.score_stride = a->score_stride;
+  p.seq_lens = a->seq_lens;
+  p.max_seq_len = a->max_seq_len;
+  p.keep = a->keep;
+  p.recent = a->recent;
+  p.first = a->first;
+  p.idx = a->idx;
+  p.counts = a->counts;
+  p.scores_out = a->scores_out;
+  p.status = d.status;
+  cudaError_t e = launch_select(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return MIMO_OK;
+}
+
+int mimo_kv_gather(const mimo_gather_args* a, void* stream) {
+  const char* fn = "mimo_kv_gather";
+  if (!a) return fail(MIMO_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  if (a->num_kv_heads != 8 && a->num_kv_heads != 4)
+    return fail(MIMO_ERR_UNSUPPORTED, "%s: num_kv_heads must be 8 or 4", fn);
+  if (a->num_seqs < 0 || a->num_seqs > 65535)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: num_seqs must be in 0..65535", fn);
+  if (a->max_pages_src <= 0 || a->num_pages_src <= 0 || a->max_pages_dst <= 0 || a->num_pages_dst <= 0)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: the page counts must be > 0", fn);
+  if (a->max_count < 0 || a->max_count > long(a->max_pages_dst) * kPage)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: max_count must be in 0..max_pages_dst * 128", fn);
+  if (a->out_dtype != a->cache_dtype && a->out_dtype != MIMO_DTYPE_BF16)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: out_dtype must be cache_dtype or MIMO_DTYPE_BF16", fn);
+  if (a->idx && a->idx_stride < a->max_count)
+    return fail(MIMO_ERR_INVALID_ARG, "%s: idx_stride is below max_count", fn);
+  const bool scaled = a->cache_dtype == MIMO_DTYPE_FP8_E4M3 && a->out_dtype == MIMO_DTYPE_BF16;
+  if (a->cache_dtype == MIMO_DTYPE_FP8_E4M3 && !scaled) {
+    // bytes move as they are: the scales play no part
+  } else if (int rc = check_cache_dtype(fn, a->cache_dtype, a->k_dequant, a->v_dequant)) {
+    return rc;
+  }
+  if (a->num_seqs == 0 || a->max_count == 0) return MIMO_OK;
+  REQUIRE_PTR(a->k_src, "k_src");
+  REQUIRE_PTR(a->v_src, "v_src");
+  REQUIRE_PTR(a->block_table_src, "block_table_src");
+  REQUIRE_PTR(a->k_dst, "k_dst");
+  REQUIRE_PTR(a->v_dst, "v_dst");
+  REQUIRE_PTR(a->block_table_dst, "block_table_dst");
+  REQUIRE_PTR(a->counts, "counts");
+  if (a->idx) REQUIRE_PTR(a->idx, "idx");
+  DevState d;
+  if (int rc = dev_state(fn, &d)) return rc;
+  GatherParams p;
+  p.num_seqs = a->num_seqs;
+  p.hkv = a->num_kv_heads;
+  p.k_src = static_cast<const uint8_t*>(a->k_src);
+  p.v_src = static_cast<const uint8_t*>(a->v_src);
+  p.table_src = a->block_table_src;
+  p.max_pages_src = a->max_pages_src;
+  p.num_pages_src = a->num_pages_src;
+  p.k_dst = static_cast<uint8_t*>(a->k_dst);
+  p.v_dst = static_cast<uint8_t*>(a->v_dst);
+  p.table_dst = a->block_table_dst;
+  p.max_pages_dst = a->max_pages_dst;
+  p.num_pages_dst = a->num_pages_dst;
+  p.counts = a->counts;
+  p.idx = a->idx;
+  p.idx_stride = a->idx_stride;
+  p.max_count = a->max_count;
+  p.cache_dtype = a->cache_dtype;
+  p.out_dtype = a->out_dtype;
+  p.k_dequant = a->k_dequant;
+  p.v_dequant = a->v_dequant;
+  p.status = d.status;
+  cudaError_t e = launch_gather(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return MIMO_OK;
 }
 
 int mimo_status_poll(uint32_t* status) {

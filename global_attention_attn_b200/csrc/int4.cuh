@@ -71,4 +71,9 @@ __device__ __forceinline__ void int4_query_group(const float* x0, const float* x
 }
 constexpr float kI4KeyUnit = 0x1p22f;  // 2^24 / 4: what a key product has to be multiplied with
 
+// The offset -8 of every code adds, per key, the sum over groups of scale * (-8 * group sum of
+// the query): one more product, whose scales are the stored fp16 pairs and whose other side
+// is -8 * sum / 128 (no query in range overflows) as two fp16 terms (k 0..5 and 8..13).
+constexpr float kI4OffsetUnit = 0x1p-15f;  // 128 * 2^-22: from that product to the key products' unit
+
 }  // namespace mimo

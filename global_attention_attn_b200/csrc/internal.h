@@ -106,6 +106,58 @@ struct Decode4Plan {
   int n_blocks, nc, groups, stages, workers, min_tiles, whole_units;
 };
 
+// Attention weights per cached slot (weights.cu).
+struct WeightsParams {
+  CUtensorMap tm_k;  // bf16 / E4M3 key rows, box {64, 1, 32}
+  int batch, hkv, q_len, max_seq_len;
+  float scale_log2;
+  const uint16_t* q;
+  const float* lse;
+  const int32_t* seq_lens;
+  const int32_t* positions;
+  const uint8_t* k_cache;
+  const int32_t* block_table;
+  int max_pages, num_pages;
+  int cache_dtype;
+  const float* k_dequant;
+  float* scores;  // [batch, hkv, score_stride]
+  long score_stride;
+  RopeFreqs rope;
+  unsigned* status;
+};
+
+// Eviction (evict.cu).
+struct SelectParams {
+  int num_seqs, hkv;
+  const float* scores;  // [num_seqs, hkv, score_stride]
+  long score_stride;
+  const int32_t* seq_lens;
+  int max_seq_len, keep, recent, first;
+  int32_t* idx;       // [num_seqs, hkv, keep]
+  int32_t* counts;    // [num_seqs]
+  float* scores_out;  // [num_seqs, hkv, keep] or null
+  unsigned* status;
+};
+struct GatherParams {
+  int num_seqs, hkv;
+  const uint8_t* k_src;
+  const uint8_t* v_src;
+  const int32_t* table_src;
+  int max_pages_src, num_pages_src;
+  uint8_t* k_dst;
+  uint8_t* v_dst;
+  const int32_t* table_dst;
+  int max_pages_dst, num_pages_dst;
+  const int32_t* counts;
+  const int32_t* idx;  // [num_seqs, hkv, idx_stride] or null (slot j from slot j)
+  long idx_stride;
+  int max_count;
+  int cache_dtype, out_dtype;
+  const float* k_dequant;
+  const float* v_dequant;
+  unsigned* status;
+};
+
 // Key source modes of the prefill kernel.
 enum PrefillMode : int {
   kModeContig = 0,  // dims 0..63 from the rotated workspace copy, 64..191 from k, v from v
@@ -188,6 +240,9 @@ void decode_rows(int q_len, int group, int* n_blocks, int* nc, int* n_rp);
 // unit_keys: keys a (sequence, KV head) covers at most
 Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms);
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end);
+cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s);
+cudaError_t launch_select(const SelectParams& p, cudaStream_t s);
+cudaError_t launch_gather(const GatherParams& p, cudaStream_t s);
 cudaError_t launch_rope_k(const RopeKParams& p, cudaStream_t s);
 // kind 0: sliding window (G=8 heads x 16 rows, one 144-key tile); kind 1: global (G=16 x 8 rows, 128-key tiles)
 // pdl: launch with programmatic stream serialization (the kernel's prologue overlaps the key

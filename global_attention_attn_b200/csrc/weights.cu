@@ -1,0 +1,449 @@
+// Attention weights per cached slot: scores[s][g][t] += sum over the draft rows i and the query
+// heads h of KV head g of exp(z_iht - lse_ih), the probabilities that the attention call whose
+// log-sum-exp is given assigned to slot t.  Their running sum over steps is what eviction by
+// accumulated weight ranks slots by.
+//
+// The keys are read once (384, 192 or 108 bytes per slot and KV head) and 8 bytes of scores:
+// no second pass for the normalisation (it is given), no exchange between tiles, no atomics (a
+// score belongs to one lane of one tile).  S^T = K Q^T on mma.sync m16n8k16: 16 keys are the
+// rows, the heads of a KV group the columns (two blocks of 8 on 4-head layers, one on 8-head
+// layers: no padding), so a key's sum over heads is four values of a thread and two shuffles.
+// A probability is compared in fp32, so the logits are kept to fp32's digits: the rotated query
+// dims, which no 16-bit type holds, enter as two fp16 terms (4 of 16 k-steps).
+//
+// One CTA takes a contiguous piece of the line of 32-key tiles of all (sequence, KV head) units;
+// its warps take the piece's tiles in turn, each with its own two stages of TMA / bulk copies,
+// and share the unit's query fragments (shared memory, up to 8 drafts).
+#include "common.cuh"
+#include "int4.cuh"
+#include "ptx.cuh"
+#include "tiles.cuh"
+#include "../../include/mimoattn.h"
+
+namespace mimo {
+
+namespace {
+
+constexpr int kTile = 32, kMaxWarps = 8, kStages = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int FMT>
+struct Fmt {  // bytes of a stage: 32 key rows (and, 4-bit, their scales)
+  static constexpr int kRow = FMT == MIMO_DTYPE_BF16 ? 384 : (FMT == MIMO_DTYPE_FP8_E4M3 ? 192 : kI4KSlot);
+  static constexpr int kStage = (kTile * kRow + 1023) / 1024 * 1024;
+  // query fragments of a draft: 12 steps, 4 remainder steps of the rotated dims, 4-bit: the offset
+  static constexpr int kSteps = FMT == MIMO_DTYPE_INT4 ? 17 : 16;
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16_acc(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_acc(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  mma_f16_c(d, a, b0, b1, d);
+}
+
+// A fragments of 16 keys for step kk.
+template <int FMT>
+__device__ __forceinline__ void key_frag(uint32_t kb, int k0, int kk, int lane, uint32_t* a) {
+  const int row = k0 + (lane & 7) + ((lane >> 3) & 1) * 8;
+  if constexpr (FMT == MIMO_DTYPE_BF16) {
+    ldsm_x4(kb + (kk >> 2) * (kTile * 128) + row * 128 + ((((kk & 3) * 2 + (lane >> 4)) ^ (row & 7)) << 4), a);
+  } else {
+    // two steps at once: bytes in pairs, 4 consecutive dims of a key per lane
+    uint32_t m[4];
+    ldsm_x4(kb + (kk >> 2) * (kTile * 64) + row * 64 + (((2 * ((kk >> 1) & 1) + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), m);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[4 * i] = f16x2_from_e4m3x2(uint16_t(m[2 * i]));
+      a[4 * i + 1] = f16x2_from_e4m3x2(uint16_t(m[2 * i + 1]));
+      a[4 * i + 2] = f16x2_from_e4m3x2(uint16_t(m[2 * i] >> 16));
+      a[4 * i + 3] = f16x2_from_e4m3x2(uint16_t(m[2 * i + 1] >> 16));
+    }
+  }
+}
+
+}  // namespace
+
+template <int FMT, int NB>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid_constant__ WeightsParams p) {
+  using F = Fmt<FMT>;
+  constexpr int G = 8 * NB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane & 3, r0 = lane >> 2;
+  const int warps = blockDim.x >> 5;
+  // stages | query fragments | cos, sin | group sums | lse | barriers | tile table
+  const uint32_t ring0 = sbase + warp * kStages * F::kStage;
+  uint32_t at = warps * kStages * F::kStage;
+  const uint32_t qf = sbase + at;
+  uint4* const qf_p = reinterpret_cast<uint4*>(smem + at);
+  at += p.q_len * F::kSteps * 512;
+  float2* const cs = reinterpret_cast<float2*>(smem + at);
+  at += p.q_len * kHalf * 8;
+  float* const sums = reinterpret_cast<float*>(smem + at);
+  at += FMT == MIMO_DTYPE_INT4 ? p.q_len * G * 8 * 4 : 0;
+  float* const lse2 = reinterpret_cast<float*>(smem + at);
+  at += p.q_len * G * 4;
+  const uint32_t bar = sbase + at + warp * kStages * 8;
+  at += kMaxWarps * kStages * 8;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + at);
+  long long* const tbl = reinterpret_cast<long long*>(smem + at + 16);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tile_table(tbl, p.batch, lane, [&](int s) {
+      const int ctx = p.seq_lens[s];
+      if ((ctx < p.q_len || ctx > p.max_seq_len) && blockIdx.x == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+      return ctx < p.q_len ? 0 : (min(ctx, p.max_seq_len) + kTile - 1) / kTile;
+    });
+  }
+  __syncthreads();
+  const long long total = tbl[p.batch] * p.hkv;
+  const long long a = blockIdx.x * total / gridDim.x, b = (blockIdx.x + 1) * total / gridDim.x;
+  if (a >= b) return;
+
+  // ---- this warp's tiles: a + warp, a + warp + warps, ...
+  auto step = [&](TileCursor& c, int n) {
+    c.t += n;
+    while (c.t >= c.nt) {
+      const int over = c.t - c.nt;
+      next_unit(tbl, p.hkv, c);
+      c.t = over;
+    }
+  };
+  TileCursor ic;
+  long long nxt = a + warp;
+  if (nxt < b) ic = cursor_at(tbl, p.batch, p.hkv, nxt);
+  int ist = 0, pg_s = -1, pg_base = 0, pg = 0;
+  auto issue = [&]() {
+    if (nxt >= b) return;
+    const int key = ic.t * kTile, pi = key / kPage;
+    if (ic.s != pg_s || pi < pg_base || pi >= pg_base + 32) {
+      pg_s = ic.s;
+      pg_base = pi;
+      const int last = (ic.nt - 1) * kTile / kPage, mine = pi + lane;
+      pg = 0;
+      if (mine <= last) {
+        pg = mine < p.max_pages ? p.block_table[long(ic.s) * p.max_pages + mine] : -1;
+        if (pg < 0 || pg >= p.num_pages) {
+          atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+          pg = 0;
+        }
+      }
+    }
+    const int page = __shfl_sync(0xffffffffu, pg, pi - pg_base), slot = key % kPage;
+    const uint32_t dst = ring0 + ist * F::kStage, br = bar + 8 * ist;
+    if (lane == 0) {
+      mbar_expect_tx(br, kTile * F::kRow);
+      if constexpr (FMT == MIMO_DTYPE_INT4) {
+        const uint8_t* kb = p.k_cache + (long(page) * p.hkv + ic.g) * (kPage * kI4KSlot);
+        bulk_load(dst, kb + slot * kI4KCodes, kTile * kI4KCodes, br);
+        bulk_load(dst + kTile * kI4KCodes, kb + kPage * kI4KCodes + slot * 2 * kI4KGroups, kTile * 2 * kI4KGroups, br);
+      } else {
+        const int row = page * kPage + slot;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) tma_load_3d(dst + i * (F::kRow / 3) * kTile, &p.tm_k, br, 64 * i, ic.g, row);
+      }
+    }
+    __syncwarp();
+    if (++ist == kStages) ist = 0;
+    nxt += warps;
+    if (nxt < b) step(ic, warps);
+  };
+  for (int i = 0; i < kStages; ++i) issue();
+
+  int st = 0, ph = 0;
+  bool ok = true;
+  TileCursor c = cursor_at(tbl, p.batch, p.hkv, a);  // the whole CTA's: the unit's first tile of the piece
+  long long x = a;
+  int mine = warp;  // this warp's next tile, counted from x
+  while (x < b) {
+    if (c.t >= c.nt) next_unit(tbl, p.hkv, c);
+    const int s = c.s, g = c.g, ctx = p.seq_lens[s], end = min(ctx, p.max_seq_len);
+    const int n = int(min((long long)(c.nt - c.t), b - x));  // tiles of this unit in the piece
+    // ---- the unit's query fragments
+    __syncthreads();  // (the last unit's are read)
+    const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
+    for (int i = threadIdx.x; i < p.q_len * kHalf; i += blockDim.x)
+      rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
+    for (int i = threadIdx.x; i < p.q_len * G; i += blockDim.x) {
+      // a row that attended nothing (or whose log-sum-exp is no number) adds nothing
+      const float l = p.lse[(long(s) * p.q_len + i / G) * kHq + g * G + i % G];
+      lse2[i] = fabsf(l) < INFINITY ? l * kLog2e : INFINITY;
+    }
+    __syncthreads();
+    const uint16_t* qg = p.q + (long(s) * p.q_len * kHq + g * G) * kDqk;
+    auto qval = [&](int i, int h, int d) {  // rotated component d of head h of draft i
+      const uint16_t* r = qg + (long(i) * kHq + h) * kDqk;
+      const float v = bf16_to_f32(r[d]);
+      if (d >= kRope) return v;
+      const float w = bf16_to_f32(r[d ^ kHalf]);
+      const float2 t = cs[i * kHalf + (d & (kHalf - 1))];
+      return d < kHalf ? v * t.x - w * t.y : v * t.x + w * t.y;
+    };
+    if constexpr (FMT == MIMO_DTYPE_INT4) {
+      for (int i = warp; i < p.q_len * G; i += warps) {
+#pragma unroll
+        for (int j = 0; j < kI4KGroups; ++j) {
+          float v = qval(i / G, i % G, kI4Group * j + lane);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (lane == 0) sums[i * 8 + j] = v;
+        }
+      }
+      __syncthreads();
+    }
+    float amax = 0.f;
+    for (int it = warp; it < p.q_len * F::kSteps; it += warps) {
+      const int i = it / F::kSteps, kq = it % F::kSteps;
+      uint32_t r[4] = {0, 0, 0, 0};  // (b0, b1) of heads r0, then of heads 8 + r0
+      const bool rest = kq >= 12 && kq < 16;
+      const int kk = rest ? kq - 12 : kq;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int h = 8 * nb + r0;
+        if (FMT == MIMO_DTYPE_INT4 && kq == 16) {
+          // the offset's product (int4.cuh): scales against -8 * group sums / 128, two fp16 terms
+          if (q4 < 3) {
+            const float c0 = sums[(i * G + h) * 8 + 2 * q4] * -0.0625f, c1 = sums[(i * G + h) * 8 + 2 * q4 + 1] * -0.0625f;
+            r[2 * nb] = pack2_f16(c0, c1);
+            const float2 t = f32x2_of_f16x2(r[2 * nb]);
+            r[2 * nb + 1] = pack2_f16(c0 - t.x, c1 - t.y);
+          }
+          continue;
+        }
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          float v[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            int d;
+            float u = 1.f;
+            if constexpr (FMT == MIMO_DTYPE_BF16) {
+              d = 16 * kk + 8 * bb + 2 * q4 + e;
+            } else if constexpr (FMT == MIMO_DTYPE_FP8_E4M3) {
+              d = 16 * kk + 4 * q4 + 2 * bb + e;
+            } else {
+              d = 32 * (kk >> 1) + 8 * q4 + 2 * (kk & 1) + bb + 4 * e;
+              u = bb ? 0.25f : 4.f;
+            }
+            v[e] = qval(i, h, d) * u;
+          }
+          if (FMT == MIMO_DTYPE_BF16 && kk >= 4) {
+            r[2 * nb + bb] = pack2_bf16(v[0], v[1]);
+          } else {
+            r[2 * nb + bb] = pack2_f16_sat(v[0], v[1], amax);
+            if (rest) {
+              const float2 t = f32x2_of_f16x2(r[2 * nb + bb]);
+              r[2 * nb + bb] = pack2_f16(v[0] - t.x, v[1] - t.y);
+            }
+          }
+        }
+      }
+      qf_p[it * 32 + lane] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
+    __syncthreads();
+
+    const float c_log2 = p.scale_log2 * (FMT == MIMO_DTYPE_FP8_E4M3 ? p.k_dequant[g] : (FMT == MIMO_DTYPE_INT4 ? kI4KeyUnit : 1.f));
+    float* const row_out = p.scores + (long(s) * p.hkv + g) * p.score_stride;
+    for (; mine < n && ok; mine += warps) {
+      const int key0 = (c.t + mine) * kTile;
+      // lane q4 < 2 adds to keys r0 + 8 q4 (+ 16): fetched before the tile is waited for
+      float old[2];
+      int slot[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        slot[m] = key0 + 16 * m + r0 + 8 * (q4 & 1);
+        old[m] = q4 < 2 && slot[m] < end ? row_out[slot[m]] : 0.f;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * st, ph & 1, abort_flag, p.status, MIMO_STATUS_TIMEOUT))) {
+        ok = false;
+        break;
+      }
+      const uint32_t kb = ring0 + st * F::kStage;
+      float add[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // keys r0, r0 + 8 of either half
+      for (int i = 0; i < p.q_len; ++i) {
+        const uint32_t qi = qf + i * F::kSteps * 512 + lane * 16;
+        float S[2][NB][4];
+        auto q_frag = [&](int kq, uint32_t* r) {
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                       : "r"(qi + kq * 512)
+                       : "memory");
+        };
+        if constexpr (FMT == MIMO_DTYPE_INT4) {
+          uint32_t r[4];
+          q_frag(16, r);
+          uint32_t sc[2][2][kI4KGroups / 2];  // scales of keys r0 and r0 + 8 of either half
+          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t aa[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t sa = kb + kTile * kI4KCodes + (16 * m + r0 + 8 * e) * 2 * kI4KGroups;
+#pragma unroll
+              for (int j = 0; j < 3; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc[m][e][j]) : "r"(sa + 4 * j) : "memory");
+              aa[e] = aa[2 + e] = q4 == 0 ? sc[m][e][0] : (q4 == 1 ? sc[m][e][1] : (q4 == 2 ? sc[m][e][2] : 0u));
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma_f16_c(S[m][nb], aa, r[2 * nb], r[2 * nb + 1], zero);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) S[m][nb][e] *= kI4OffsetUnit;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kI4KGroups; ++j) {
+            float d[2][NB][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              uint32_t rr[4];
+              q_frag(2 * j + t, r);
+              if (j < 2) q_frag(12 + 2 * j + t, rr);
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                uint32_t w0, w1;
+                const uint32_t ka = kb + (16 * m + r0) * kI4KCodes + 24 * q4 + 4 * j;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w0) : "r"(ka) : "memory");
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w1) : "r"(ka + 8 * kI4KCodes) : "memory");
+                const uint32_t y0 = t ? w0 >> 8 : w0, y1 = t ? w1 >> 8 : w1;
+                const uint32_t aa[4] = {y0 & kI4Lo, y1 & kI4Lo, y0 & kI4Hi, y1 & kI4Hi};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  if (t == 0) mma_f16_c(d[m][nb], aa, r[2 * nb], r[2 * nb + 1], zero);
+                  else mma_f16_acc(d[m][nb], aa, r[2 * nb], r[2 * nb + 1]);
+                  if (j < 2) mma_f16_acc(d[m][nb], aa, rr[2 * nb], rr[2 * nb + 1]);
+                }
+              }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const float2 t0 = f32x2_of_f16x2(sc[m][0][j >> 1]), t1 = f32x2_of_f16x2(sc[m][1][j >> 1]);
+              const float s0 = (j & 1) ? t0.y : t0.x, s1 = (j & 1) ? t1.y : t1.x;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                S[m][nb][0] = fmaf(d[m][nb][0], s0, S[m][nb][0]);
+                S[m][nb][1] = fmaf(d[m][nb][1], s0, S[m][nb][1]);
+                S[m][nb][2] = fmaf(d[m][nb][2], s1, S[m][nb][2]);
+                S[m][nb][3] = fmaf(d[m][nb][3], s1, S[m][nb][3]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) S[m][nb][0] = S[m][nb][1] = S[m][nb][2] = S[m][nb][3] = 0.f;
+          constexpr int kPer = FMT == MIMO_DTYPE_BF16 ? 1 : 2;  // steps a key fragment load covers
+#pragma unroll
+          for (int k2 = 0; k2 < 12; k2 += kPer) {
+            uint32_t ka[2][4 * kPer];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) key_frag<FMT>(kb, 16 * m, k2, lane, ka[m]);
+#pragma unroll
+            for (int t = 0; t < kPer; ++t) {
+              const int kk = k2 + t;
+              uint32_t r[4], rr[4];
+              q_frag(kk, r);
+              if (kk < 4) q_frag(12 + kk, rr);
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  if (FMT == MIMO_DTYPE_BF16 && kk >= 4) mma_bf16_acc(S[m][nb], ka[m] + 4 * t, r[2 * nb], r[2 * nb + 1]);
+                  else mma_f16_acc(S[m][nb], ka[m] + 4 * t, r[2 * nb], r[2 * nb + 1]);
+                  if (kk < 4) mma_f16_acc(S[m][nb], ka[m] + 4 * t, rr[2 * nb], rr[2 * nb + 1]);
+                }
+            }
+          }
+        }
+        // heads 8 nb + 2 q4, + 1
+        const int last = min(end - 1, ctx - p.q_len + i);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float2 l = *reinterpret_cast<const float2*>(lse2 + i * G + 8 * nb + 2 * q4);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const float v0 = ex2(fmaf(S[m][nb][0], c_log2, -l.x)) + ex2(fmaf(S[m][nb][1], c_log2, -l.y));
+            const float v1 = ex2(fmaf(S[m][nb][2], c_log2, -l.x)) + ex2(fmaf(S[m][nb][3], c_log2, -l.y));
+            if (key0 + 16 * m + r0 <= last) add[m][0] += v0;
+            if (key0 + 16 * m + r0 + 8 <= last) add[m][1] += v1;
+          }
+        }
+      }
+      __syncwarp();
+      issue();  // the stage is read
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          add[m][e] += __shfl_xor_sync(0xffffffffu, add[m][e], 1);
+          add[m][e] += __shfl_xor_sync(0xffffffffu, add[m][e], 2);
+        }
+        if (q4 < 2 && slot[m] < end) row_out[slot[m]] = old[m] + (q4 ? add[m][1] : add[m][0]);
+      }
+      if (++st == kStages) st = 0, ++ph;
+    }
+    // (a wait that ran out: the warp goes on to the next barriers with nothing to do)
+    mine -= n;
+    if (!ok) mine = 0x3fffffff;
+    c.t += n;
+    x += n;
+  }
+  if (!ok && lane == 0) {
+    // the copies under way land before the warp leaves: the stage waited for, and the one after it
+    int dummy = 0;
+    const long long done = nxt - warps;  // the last tile that was issued
+    mbar_wait(bar + 8 * st, ph & 1, &dummy, nullptr, 0, 50000000ull);
+    if (done >= a + warp + warps) mbar_wait(bar + 8 * (st ^ 1), (ph + (st == 1 ? 1 : 0)) & 1, &dummy, nullptr, 0, 50000000ull);
+  }
+}
+
+namespace {
+template <int FMT>
+int smem_of(int warps, int q_len, int hkv) {
+  const int G = kHq / hkv;
+  return 1024 + warps * kStages * Fmt<FMT>::kStage + q_len * (Fmt<FMT>::kSteps * 512 + kHalf * 8 + G * 4 + (FMT == MIMO_DTYPE_INT4 ? G * 32 : 0)) +
+         kMaxWarps * kStages * 8 + 16 + (kTableMaxBatch + 1) * 8;
+}
+template <int FMT, int NB>
+cudaError_t launch_weights_fmt(const WeightsParams& p, int sms, cudaStream_t s) {
+  int warps = kMaxWarps;  // as many as their stages fit beside the drafts' fragments
+  while (smem_of<FMT>(warps, p.q_len, p.hkv) > 232448) --warps;
+  const int bytes = smem_of<FMT>(warps, p.q_len, p.hkv);
+  cudaError_t e = cudaFuncSetAttribute(weights_kernel<FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const long long tiles = ((long long)p.max_seq_len + kTile - 1) / kTile * p.batch * p.hkv;
+  weights_kernel<FMT, NB><<<int(tiles < sms ? tiles : sms), warps * 32, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s) {
+  switch (p.cache_dtype * 2 + (p.hkv == 8)) {
+    case MIMO_DTYPE_BF16 * 2: return launch_weights_fmt<MIMO_DTYPE_BF16, 2>(p, sms, s);
+    case MIMO_DTYPE_BF16 * 2 + 1: return launch_weights_fmt<MIMO_DTYPE_BF16, 1>(p, sms, s);
+    case MIMO_DTYPE_FP8_E4M3 * 2: return launch_weights_fmt<MIMO_DTYPE_FP8_E4M3, 2>(p, sms, s);
+    case MIMO_DTYPE_FP8_E4M3 * 2 + 1: return launch_weights_fmt<MIMO_DTYPE_FP8_E4M3, 1>(p, sms, s);
+    case MIMO_DTYPE_INT4 * 2: return launch_weights_fmt<MIMO_DTYPE_INT4, 2>(p, sms, s);
+    default: return launch_weights_fmt<MIMO_DTYPE_INT4, 1>(p, sms, s);
+  }
+}
+
+}  // namespace mimo

@@ -376,6 +376,108 @@ typedef struct {
 
 MIMO_API int mimo_kv_append(const mimo_append_args* args, void* stream);
 
+/*
+ * Attention weights per cached slot of a paged cache (global layers: no window):
+ *   scores[s][g][t] += sum over draft rows i and query heads h of KV head g of
+ *                      exp(softmax_scale * q_ih . k_t - lse_ih),
+ * the probabilities that an attention call with this log-sum-exp gave slot t (rows i that
+ * do not see t add nothing).  Summed over decode steps they are the accumulated attention
+ * weights that mimo_kv_select ranks slots by.  No page describes this call or the two after
+ * it; they serve contexts that outgrow their cache.
+ *
+ * q and lse are a mimo_attn_decode call's (same rows, seq_lens, positions; lse with its sink,
+ * so that layer.sink is not read here; a row whose lse is not finite adds nothing).  scores:
+ * fp32 [batch, num_kv_heads, score_stride], slots 0 .. seq_lens[s] - 1 of each row are read
+ * and written, the others left alone.  layer.window must be 0.  The keys are read once, in
+ * any cache format; values are not.  Deterministic: no atomics.
+ */
+typedef struct {
+  mimo_layer layer;
+  int batch;
+  int q_len;                  /* query tokens per sequence: 0 or 1, up to MIMO_MAX_DRAFTS */
+  int max_seq_len;            /* upper bound of seq_lens; score_stride >= max_seq_len */
+  const void* q;              /* [batch * q_len, 64, 192] bf16 pre-RoPE */
+  const float* lse;           /* [batch * q_len, 64] fp32 */
+  const int32_t* seq_lens;    /* device int32 [batch] */
+  const int32_t* positions;   /* device int32 [batch] rotary positions, or NULL (seq_lens - 1) */
+  const void* k_cache;
+  const int32_t* block_table; /* device int32 [batch, max_pages] */
+  int max_pages;
+  int num_pages;
+  int cache_dtype;
+  const float* k_dequant;     /* FP8: device fp32 [num_kv_heads], else NULL */
+  float* scores;
+  int score_stride;
+} mimo_weights_args;
+
+MIMO_API int mimo_attn_weights(const mimo_weights_args* args, void* stream);
+
+/*
+ * Selection of the slots that stay.  Of a sequence's seq_lens[s] slots each KV head keeps
+ * min(seq_lens[s], keep): the first `first` and the last `recent` ones, and of the others
+ * those with the largest scores (equal scores: the lowest slot; -0 equals 0, NaN counts as
+ * -infinity).  first + recent <= keep; max_seq_len <= MIMO_SELECT_MAX_SLOTS.
+ *   idx [num_seqs, num_kv_heads, keep] int32: the kept slots, ascending, then -1;
+ *   counts [num_seqs] int32: how many;
+ *   scores_out [num_seqs, num_kv_heads, keep] fp32 (or NULL): their scores, then 0.  It must
+ *   not overlap scores.
+ * A seq_lens outside 0 .. max_seq_len sets MIMO_STATUS_BAD_INDEX and counts as the nearer bound.
+ */
+#define MIMO_SELECT_MAX_SLOTS 393216
+typedef struct {
+  int num_seqs;
+  int num_kv_heads;
+  const float* scores; /* fp32 [num_seqs, num_kv_heads, score_stride] */
+  int score_stride;    /* >= max_seq_len */
+  const int32_t* seq_lens;
+  int max_seq_len;
+  int keep;
+  int recent;
+  int first;
+  int32_t* idx;
+  int32_t* counts;
+  float* scores_out;
+} mimo_select_args;
+
+MIMO_API int mimo_kv_select(const mimo_select_args* args, void* stream);
+
+/*
+ * Gather of cache slots into other pages: slot j < counts[s] of sequence s and KV head g in the
+ * destination gets the key and value of source slot idx[s][g][j] (idx NULL: of slot j).  The
+ * destination has the source's format (an eviction's compaction; whole pages moved) or, for an
+ * E4M3 or 4-bit source, is a bf16 cache: the values the codes stand for, rounded once (key
+ * dims 0..63 to fp16), as prefill over a stored prefix reads them.  Keys keep the rotation they
+ * were appended with: decode passes `positions`, append `slots` afterwards.
+ * No page may be both read and written by one call: evict into fresh pages and release the old
+ * ones (pages shared between sequences stay whole).  Destination slots from counts[s] on are
+ * left as they were.  A slot or page outside its table or cache sets MIMO_STATUS_BAD_INDEX and
+ * is skipped; counts[s] above max_count is cut to it and reported.
+ */
+typedef struct {
+  int num_seqs;
+  int num_kv_heads;
+  const void* k_src;
+  const void* v_src;
+  const int32_t* block_table_src; /* device int32 [num_seqs, max_pages_src] */
+  int max_pages_src;
+  int num_pages_src;
+  void* k_dst;
+  void* v_dst;
+  const int32_t* block_table_dst; /* device int32 [num_seqs, max_pages_dst] */
+  int max_pages_dst;
+  int num_pages_dst;
+  const int32_t* counts;          /* device int32 [num_seqs] */
+  const int32_t* idx;             /* device int32 [num_seqs, num_kv_heads, idx_stride], or NULL */
+  int idx_stride;                 /* >= max_count when idx is given */
+  int max_count;                  /* host-side upper bound of counts; <= max_pages_dst * 128 */
+  int cache_dtype;                /* the source's format */
+  int out_dtype;                  /* the same, or MIMO_DTYPE_BF16 */
+  const float* k_dequant;         /* E4M3 -> bf16: device fp32 [num_kv_heads], else NULL */
+  const float* v_dequant;
+} mimo_gather_args;
+
+MIMO_API int mimo_kv_gather(const mimo_gather_args* args, void* stream);
+
 /* Thread-local message for the last error returned on this thread. */
 MIMO_API const char* mimo_last_error(void);
 

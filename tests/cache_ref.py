@@ -81,8 +81,10 @@ def rotate(x, pos, base):
 class Row:
     """One sequence's attention: keys / values float64 [Hkv, n, dims] at slot positions `at`."""
 
-    def __init__(self, q, k, v, at, me, base, *, pos=None, window=0, sink=None, v_scale=M.V_SCALE, q_fp16=True):
-        """q [q_len, 64, 192]; me [q_len] slot of each query row; pos [q_len] its rotary position."""
+    def __init__(self, q, k, v, at, me, base, *, pos=None, window=0, sink=None, v_scale=M.V_SCALE, p_step=2.0 ** -10):
+        """q [q_len, 64, 192]; me [q_len] slot of each query row; pos [q_len] its rotary position; p_step:
+        what a weight's rounding is off by (fp16 twice: 2 x 2^-11; bf16: 2^-8)."""
+        self.p_step = p_step
         hkv = k.shape[0]
         qr = rotate(q, me if pos is None else pos, base).view(len(me), hkv, 64 // hkv, 192)
         z = torch.einsum("ihgd,htd->ihgt", qr, k) * SCALE
@@ -105,10 +107,10 @@ class Row:
     def check(self, out, lse, what=""):
         """bf16 output within half a step of its own plus what the kernel's roundings can do: a
         logit error moves every weight by it, twice (numerator and sum); a weight is rounded to
-        fp16 twice (2 x 2^-11); the fp32 sums of weight * code, codes up to 15 against a
+        a narrow type once or twice (p_step); the fp32 sums of weight * code, codes up to 15 against a
         largest value of 7, keep 2^-14 of the grid's size."""
         err = (out.double() - self.out).abs()
-        tol = 2.0 ** -8 * self.out.abs() + (2 * self.dz + 2.0 ** -10) * self.mean_abs + 2.0 ** -14 * self.grid
+        tol = 2.0 ** -8 * self.out.abs() + (2 * self.dz + self.p_step) * self.mean_abs + 2.0 ** -14 * self.grid
         worst = float((err / tol).max())
         assert torch.isfinite(out).all() and worst <= 1, f"{what}: output off by {worst:.3g} of its bound"
         if lse is not None:
