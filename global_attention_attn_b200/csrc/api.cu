@@ -230,7 +230,7 @@ size_t decode4_workspace(const Decode4Plan& d, int batch) {
   if (d.whole_units) return 0;
   const size_t rows = 2 * size_t(d.workers) * d.n_blocks * 16;
   return round256(rows * kDv * 4) + round256(rows * 2 * 4) +
-         round256((size_t(batch < kI4MaxBatch ? batch : kI4MaxBatch) + 1) * 8);
+         round256((size_t(batch < kMaxTableBatch ? batch : kMaxTableBatch) + 1) * 8);
 }
 // The plan never counts on more SMs than this, so that the size query needs no device.
 constexpr int kI4Sms = 148;
@@ -245,7 +245,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   const int hkv = a->layer.num_kv_heads;
   Decode4Params p;
   std::memset(&p, 0, sizeof(p));
-  Decode4Plan plan = decode4_plan(a->batch < kI4MaxBatch ? a->batch : kI4MaxBatch, hkv, q_len,
+  Decode4Plan plan = decode4_plan(a->batch < kMaxTableBatch ? a->batch : kMaxTableBatch, hkv, q_len,
                                   ring ? ring_slots : decode_unit_keys(a->max_seq_len, a->layer.window, q_len), ring,
                                   d.sms < kI4Sms ? d.sms : kI4Sms);
   while (plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
@@ -256,7 +256,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
     const cuuint64_t blocks = cuuint64_t(ring ? a->batch : a->num_pages) * hkv;
     cuuint64_t gdim[3] = {64, slots, blocks};
     cuuint64_t gstride[2] = {64, slots * MIMO_INT4_V_SLOT_BYTES};
-    cuuint32_t box[3] = {64, kI4Tile, 1};
+    cuuint32_t box[3] = {64, cuuint32_t(plan.tile), 1};
     cuuint32_t estride[3] = {1, 1, 1};
     CUresult r = enc(&p.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a->v_cache), gdim, gstride, box,
                      estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
@@ -267,6 +267,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   p.group = kHq / hkv;
   p.q_len = q_len;
   p.n_blocks = plan.n_blocks;
+  p.one = plan.one;
   p.nc = plan.nc;
   p.groups = plan.groups;
   p.stages = plan.stages;
@@ -292,10 +293,10 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
     p.ws_tbl = reinterpret_cast<long long*>(ws + round256(rows * kDv * 4) + round256(rows * 2 * 4));
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // launches of at most kI4MaxBatch sequences, which follow each other on the stream and share
+  // launches of at most kMaxTableBatch sequences, which follow each other on the stream and share
   // the workspace
-  for (int s0 = 0; s0 < a->batch; s0 += kI4MaxBatch) {
-    p.batch = a->batch - s0 < kI4MaxBatch ? a->batch - s0 : kI4MaxBatch;
+  for (int s0 = 0; s0 < a->batch; s0 += kMaxTableBatch) {
+    p.batch = a->batch - s0 < kMaxTableBatch ? a->batch - s0 : kMaxTableBatch;
     p.q = static_cast<const uint16_t*>(a->q) + long(s0) * q_len * kHq * kDqk;
     p.seq_lens = a->seq_lens + s0;
     p.positions = a->positions ? a->positions + s0 : nullptr;
@@ -305,7 +306,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
     p.block0 = ring ? long(s0) * hkv : 0;
     p.out = static_cast<uint16_t*>(a->out) + long(s0) * q_len * kHq * kDv;
     p.lse = a->lse ? a->lse + long(s0) * q_len * kHq : nullptr;
-    const bool last = s0 + kI4MaxBatch >= a->batch;
+    const bool last = s0 + kMaxTableBatch >= a->batch;
     cudaError_t e = launch_decode4(p, d.sms, st, s0 == 0 ? a->ev_kernel_begin : nullptr, last ? a->ev_kernel_end : nullptr);
     if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   }
@@ -450,7 +451,7 @@ size_t mimo_attn_decode_int4_workspace_size(int batch, int q_len, int max_seq_le
   if (batch <= 0 || max_seq_len <= 0 || q_len < 1 || q_len > MIMO_MAX_DRAFTS || (num_kv_heads != 8 && num_kv_heads != 4) ||
       window < 0 || cache_kind != MIMO_CACHE_PAGED)
     return 0;
-  return decode4_workspace(decode4_plan(batch < kI4MaxBatch ? batch : kI4MaxBatch, num_kv_heads, q_len,
+  return decode4_workspace(decode4_plan(batch < kMaxTableBatch ? batch : kMaxTableBatch, num_kv_heads, q_len,
                                         decode_unit_keys(max_seq_len, window, q_len), false, kI4Sms),
                            batch);
 }
@@ -921,8 +922,8 @@ int mimo_attn_weights(const mimo_weights_args* a, void* stream) {
   p.score_stride = a->score_stride;
   p.rope = make_freqs(a->layer.rope_base);
   p.status = d.status;
-  for (int s0 = 0; s0 < a->batch; s0 += kI4MaxBatch) {
-    p.batch = a->batch - s0 < kI4MaxBatch ? a->batch - s0 : kI4MaxBatch;
+  for (int s0 = 0; s0 < a->batch; s0 += kMaxTableBatch) {
+    p.batch = a->batch - s0 < kMaxTableBatch ? a->batch - s0 : kMaxTableBatch;
     p.q = static_cast<const uint16_t*>(a->q) + long(s0) * q_len * kHq * kDqk;
     p.lse = a->lse + long(s0) * q_len * kHq;
     p.seq_lens = a->seq_lens + s0;

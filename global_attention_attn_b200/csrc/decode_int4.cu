@@ -1,20 +1,24 @@
-// Decode and draft verification over a 4-bit cache (ring or paged): the attention of decode.cu
-// on the cache format of int4.cuh.
+// Decode over a 4-bit ring and draft verification (2..8 query tokens per sequence) over a 4-bit
+// ring or paged cache: the attention of decode.cu on the cache format of int4.cuh; the paged
+// one-token decode's host side (decode_int4_tc.cu) and the combine kernel of both.
 //
-// 180 bytes per (key, KV head) stand against 16 x 320 multiply-adds (a global layer's 16 query
-// heads), 57 FLOP per byte, and every element has to be unpacked first: unlike the wide caches
-// this one is bound by instruction issue and mma.sync, and the kernel is laid out to spend as
-// few instructions per element as it can:
-//   - unpacking is one shift and four ANDs per 8 elements (int4.cuh); the key offset is the
-//     start value of a group's accumulator, and a group's scale multiplies its 16 x 8 products
-//     in fp32 (packed pairs), not its 32 x 8 elements;
+// 180 bytes per (key, KV head) stand against 16 x 320 multiply-adds a draft (57 FLOP per byte),
+// and every element has to be unpacked first: unlike the wide caches this one is bound by
+// instruction issue and mma.sync, and the kernel is laid out to spend as few instructions per
+// element as it can:
+//   - unpacking is one shift and four ANDs per 8 elements (int4.cuh); the key offset is one
+//     product per 8 keys, and a group's scale multiplies its 16 x 8 products in fp32, not its
+//     32 x 8 elements;
 //   - a value's scale is moved into the probabilities (fp16 pairs), its transposed fragments
 //     come from ldmatrix.trans: a 16-bit element of the transposed matrix is 4 dims of a key,
 //     so a register is 4 dims of a key pair, ready for the same masks;
-//   - the value offset is one more product per group of dims, p against a constant.  A sum of
-//     p * code over tens of thousands of keys would grow far above the result and lose it to
-//     the accumulator's rounding; so the odd key of each pair enters as -p * (15 - code) (the
-//     complement is free in the mask's LOP3) and the sum stays near zero on the way.
+//   - the value offset is one more product per group of dims, p against a constant in the
+//     columns of that group (the groups share an accumulator).  A sum of p * code over tens of
+//     thousands of keys would grow far above the result and lose it to the accumulator's
+//     rounding; so the odd key of each pair enters as -p * (15 - code) (the complement is free
+//     in the mask's LOP3) and the sum stays near zero on the way;
+//   - the rotated query dims enter as two fp16 terms: no 16-bit type holds them to the digits of
+//     an fp32 log-sum-exp.
 //
 // Workers are groups of nc warps (one per 16-row block of query rows, sharing the tiles).  The
 // tiles (32 keys) of all sequences and KV heads form one line, cut into as many equal pieces
@@ -29,6 +33,7 @@
 #include "common.cuh"
 #include "int4.cuh"
 #include "ptx.cuh"
+#include "tiles.cuh"
 #include "../../include/mimoattn.h"
 
 namespace mimo {
@@ -36,6 +41,7 @@ namespace mimo {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kCombineWarps = 4;
 constexpr int kTile = kI4Tile;
 // stage: value codes (64-byte swizzle), key codes, key scales, value scales
 constexpr int kOffK = kTile * kI4VCodes, kOffKs = kOffK + kTile * kI4KCodes;
@@ -43,20 +49,16 @@ constexpr int kOffVs = kOffKs + kTile * 2 * kI4KGroups;
 constexpr int kStage = 6144;
 static_assert(kOffVs + kTile * 2 * kI4VGroups <= kStage && kStage % 1024 == 0, "stage layout");
 constexpr int kAllStages = 32;
-constexpr int kOffBar = kAllStages * kStage;
+constexpr int kOffRest = kAllStages * kStage;  // a warp's second terms of the rotated dims: 4 steps x 512 bytes
+constexpr int kOffBar = kOffRest + kWarps * 2048;
 constexpr int kOffTbl = kOffBar + 2 * kAllStages * 8 + 16;
-constexpr int kSmem = kOffTbl + (kI4MaxBatch + 1) * 8 + 1024;
+constexpr int kSmem = kOffTbl + (kMaxTableBatch + 1) * 8 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // probabilities are kept as 2^kPBias * p: products with small value scales stay clear of
 // fp16's subnormals (and 2^6 * 1023, the largest scale an append stores, below its limit)
 constexpr float kPBias = 6.f;
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -67,6 +69,20 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
 }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* r) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t a;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr));
+  return a;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* r) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+// two floats -> fp16x2, one instruction
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -94,43 +110,6 @@ __device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
   return u;
 }
 
-// The line of tiles: sequence s's heads hold hkv * (tbl[s + 1] - tbl[s]) of them.  A position
-// on it, resolved.
-struct Cursor {
-  int s, g, t, nt;
-};
-__device__ __forceinline__ Cursor cursor_at(const long long* tbl, int batch, int hkv, long long x) {
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tbl[mid] * hkv <= x) lo = mid;
-    else hi = mid;
-  }
-  Cursor c;
-  c.s = lo;
-  c.nt = int(tbl[lo + 1] - tbl[lo]);
-  const long long rem = x - tbl[lo] * hkv;
-  c.g = int(rem / c.nt);
-  c.t = int(rem - (long long)c.g * c.nt);
-  return c;
-}
-// The next unit that has tiles (the caller knows there is one).
-__device__ __forceinline__ void next_unit(const long long* tbl, int hkv, Cursor& c) {
-  c.t = 0;
-  if (++c.g < hkv) return;
-  c.g = 0;
-  do {
-    ++c.s;
-    c.nt = int(tbl[c.s + 1] - tbl[c.s]);
-  } while (c.nt == 0);
-}
-
-// Workers that get a piece, and where a piece begins.
-__device__ __forceinline__ int workers_of(const Decode4Params& p, long long total) {
-  const long long w = (total + p.min_tiles - 1) / p.min_tiles;
-  return int(w < p.workers ? w : p.workers);
-}
-
 }  // namespace
 
 __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_constant__ Decode4Params p) {
@@ -155,29 +134,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     fence_mbar_init();
   }
   if (warp == kWarps - 1) {
-    long long carry = 0;
-    if (lane == 0) tbl[0] = 0;
-    for (int base = 0; base < p.batch; base += 32) {
-      const int s = base + lane;
-      long long n = 0;
-      if (s < p.batch) {
-        const int ctx = p.seq_lens[s];
-        if (ctx < p.q_len || (ctx > p.max_seq_len && p.cache_kind != MIMO_CACHE_RING))
-          atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-        n = span_of(p, ctx).nt;
-      }
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, n, d);
-        if (lane >= d) n += u;
-      }
-      if (s < p.batch) tbl[s + 1] = carry + n;
-      carry += __shfl_sync(0xffffffffu, n, 31);
-    }
-    if (blockIdx.x == 0 && p.ws_tbl) {
-      __syncwarp();
+    tile_table(tbl, p.batch, lane, [&](int s) {
+      const int ctx = p.seq_lens[s];
+      if (blockIdx.x == 0 && (ctx < p.q_len || (ctx > p.max_seq_len && p.cache_kind != MIMO_CACHE_RING)))
+        atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+      return span_of(p, ctx).nt;
+    });
+    if (blockIdx.x == 0 && p.ws_tbl)
       for (int s = lane; s <= p.batch; s += 32) p.ws_tbl[s] = tbl[s];
-    }
   }
   __syncthreads();
   if (grp >= p.groups) return;
@@ -197,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     a = at(w * units / W);
     b = at((w + 1) * units / W);
   } else {
-    const int W = workers_of(p, total);
+    const int W = pieces_of(total, p.min_tiles, p.workers);
     if (w >= W) return;
     a = w * total / W;
     b = (w + 1) * total / W;
@@ -212,18 +176,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
   };
 
   // ---- the leader's side: copies of the tiles a .. b - 1 in order
-  const Cursor start = cursor_at(tbl, p.batch, p.hkv, a);
-  Cursor ic = start;
-  long long issued = a;
+  const TileCursor start = cursor_at(tbl, p.batch, p.hkv, a);
+  TileCursor ic = start;
+  int left = int(b - a);
   int ist = 0, iph = 0;         // stage and pass of the next copy
   int pg_s = -1, pg_base = 0, pg = 0, it0 = 0;  // lane i: page id of page pg_base + i of sequence pg_s
+  // what lanes 0..3 copy: key codes, key scales, value scales (bulk copies), value codes (a TMA tile)
+  const int lane_bytes = lane == 0 ? kI4KCodes : (lane == 1 ? 2 * kI4KGroups : 2 * kI4VGroups);
+  const uint32_t lane_dst = lane == 0 ? kOffK : (lane == 1 ? kOffKs : kOffVs);
+  const int lane_block = slots * (lane < 2 ? kI4KSlot : kI4VSlot);
+  const uint8_t* const lane_src =
+      lane == 0 ? p.k_cache : (lane == 1 ? p.k_cache + slots * kI4KCodes : p.v_cache + slots * kI4VCodes);
   auto issue = [&]() -> bool {
-    if (issued >= b) return true;
+    if (left == 0) return true;
+    --left;
     if (ic.t == ic.nt) next_unit(tbl, p.hkv, ic);
-    long block;
-    int slot;
+    int block, slot;
     if (ring) {
-      block = p.block0 + long(ic.s) * p.hkv + ic.g;
+      block = int(p.block0) + ic.s * p.hkv + ic.g;
       slot = ic.t * kTile;
     } else {
       if (ic.s != pg_s) it0 = span_of(p, p.seq_lens[ic.s]).t0;
@@ -241,24 +211,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
           }
         }
       }
-      block = long(__shfl_sync(0xffffffffu, pg, pi - pg_base)) * p.hkv + ic.g;
+      block = __shfl_sync(0xffffffffu, pg, pi - pg_base) * p.hkv + ic.g;
       slot = key % kPage;
     }
     if (nc > 1 && iph > 0 && !wait_w(empty(ist), (iph - 1) & 1)) return false;
     const int n = min(kTile, slots - slot);
     const uint32_t dst = ring0 + ist * kStage, bar = full(ist);
-    if (lane == 0) {
-      mbar_expect_tx(bar, n * (kI4KSlot + 2 * kI4VGroups) + kTile * kI4VCodes);
-      const uint8_t* kb = p.k_cache + block * (long(slots) * kI4KSlot);
-      const uint8_t* vb = p.v_cache + block * (long(slots) * kI4VSlot);
-      bulk_load(dst + kOffK, kb + slot * kI4KCodes, n * kI4KCodes, bar);
-      bulk_load(dst + kOffKs, kb + slots * kI4KCodes + slot * 2 * kI4KGroups, n * 2 * kI4KGroups, bar);
-      bulk_load(dst + kOffVs, vb + slots * kI4VCodes + slot * 2 * kI4VGroups, n * 2 * kI4VGroups, bar);
-      tma_load_3d(dst, &p.tm_v, bar, 0, slot, int(block));
-    }
+    if (lane == 0) mbar_expect_tx(bar, n * (kI4KSlot + 2 * kI4VGroups) + kTile * kI4VCodes);
+    __syncwarp();
+    if (lane < 3) bulk_load(dst + lane_dst, lane_src + (long(block) * lane_block + slot * lane_bytes), n * lane_bytes, bar);
+    else if (lane == 3) tma_load_3d(dst, &p.tm_v, bar, 0, slot, block);
     __syncwarp();
     ++ic.t;
-    ++issued;
     if (++ist == stages) ist = 0, ++iph;
     return true;
   };
@@ -277,14 +241,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
 
   // ---- every warp's side
   const int q4 = lane & 3, r0 = lane >> 2;
+  const uint32_t rest0 = sbase + kOffRest + warp * 2048 + lane * 16;
   const int G = p.group, rows = p.n_blocks * 16;
   int st = 0, ph = 0;
   bool behind = false;  // nc > 1: a stage was released but its next copy is not issued yet
-  Cursor c = start;
-  for (long long x = a; x < b && ok;) {
+  TileCursor c = start;
+  const int n_all = int(b - a);
+  for (int x = 0; x < n_all && ok;) {
     if (c.t == c.nt) next_unit(tbl, p.hkv, c);
     const int s = c.s, g = c.g, t_first = c.t;
-    const int t_end = int(min((long long)c.nt, c.t + (b - x)));
+    const int t_end = min(c.nt, c.t + (n_all - x));
     const int ctx = p.seq_lens[s];
     const Span U = span_of(p, ctx);
     // rows r0 and r0 + 8 of the block: row 16 blk + r is draft (16 blk + r) / G
@@ -298,9 +264,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
       lo_r[hf] = valid ? (p.window > 0 ? max(0, at - p.window + 1) : 0) : lo_r[0];
       hi_r[hf] = valid ? min(U.end - 1, at) : hi_r[0];
     }
-    // ---- query fragments and the key accumulators' start values
+    // ---- query fragments (the second terms in shared memory), and those of the key offset's product
     uint32_t qa[2 * kI4KGroups][4];
-    float ck[kI4KGroups][2];
+    uint32_t off[4] = {0u, 0u, 0u, 0u};
     {
       float cs[2], sn[2];
       const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
@@ -346,13 +312,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
           v[hf][1][i] = yy * ci + xx * si;
         }
       }
-      int4_query_group(v[0][0], v[1][0], qa, ck[0][0], ck[0][1], amax);
-      int4_query_group(v[0][1], v[1][1], qa + 2, ck[1][0], ck[1][1], amax);
+      auto group = [&](int j, const float* x0, const float* x1) {
+        uint32_t rest[2][4];
+        int4_query_group(x0, x1, qa + 2 * j, rest, amax);
+        if (j < 2) {
+          sts128(rest0 + 1024 * j, rest[0]);
+          sts128(rest0 + 1024 * j + 512, rest[1]);
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[0] += x0[i];
+          sum[1] += x1[i];
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+        }
+        int4_offset_group(off, j, q4, sum[0], sum[1]);
+      };
+      group(0, v[0][0], v[1][0]);
+      group(1, v[0][1], v[1][1]);
 #pragma unroll
       for (int j = 2; j < kI4KGroups; ++j) {
         widen(raw[0][j], v[0][0]);
         widen(raw[1][j], v[1][0]);
-        int4_query_group(v[0][0], v[1][0], qa + 2 * j, ck[j][0], ck[j][1], amax);
+        group(j, v[0][0], v[1][0]);
       }
       if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
     }
@@ -361,12 +347,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     const int ring_off = ring ? ((R - ctx) % R + R) % R : 0;  // slot j holds position ctx - R + (j + ring_off) % R
     const int lo_all = max(lo_r[0], lo_r[1]), hi_all = min(hi_r[0], hi_r[1]);
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
-    float o[kI4VGroups][4][4], T[kI4VGroups][4];
+    float o[kI4VGroups][4][4], T[4] = {0.f, 0.f, 0.f, 0.f};  // T: column n holds group n % 4's offset
+    uint32_t tb[kI4VGroups];  // (-8, -7) in the columns of group u, else 0
 #pragma unroll
     for (int u = 0; u < kI4VGroups; ++u) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[u][e][0] = o[u][e][1] = o[u][e][2] = o[u][e][3] = 0.f;
-      T[u][0] = T[u][1] = T[u][2] = T[u][3] = 0.f;
+      tb[u] = (r0 & 3) == u ? 0xC700C800u : 0u;
     }
 
     for (; c.t < t_end; ++c.t, ++x) {
@@ -375,6 +362,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
         const uint32_t vb = ring0 + st * kStage, kb = vb + kOffK, ksb = vb + kOffKs, vsb = vb + kOffVs;
         // ---- S = Q K^T, 8 keys at a time
         float S[4][4];
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
           uint32_t kw[6], kh[6];
@@ -385,23 +373,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
             lds64(ka + 8 * i, kw[2 * i], kw[2 * i + 1]);
             lds64(sa + 8 * i, kh[2 * i], kh[2 * i + 1]);
           }
-          uint64_t s01 = 0, s23 = 0;
+          // groups 2 q4, 2 q4 + 1 of key r0 (lane 3 of a quad: k 6, 7, which are none)
+          uint32_t ob = lds32(ksb + (8 * nb + r0) * 2 * kI4KGroups + 4 * min(q4, 2));
+          ob = q4 == 3 ? 0u : ob;
+          mma_f16_c(S[nb], off, ob, ob, zero);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[nb][e] *= kI4OffsetUnit;
 #pragma unroll
           for (int j = 0; j < kI4KGroups; ++j) {
             const uint32_t wd = kw[j], w8 = wd >> 8;
-            const float c0[4] = {ck[j][0], ck[j][0], ck[j][1], ck[j][1]};
+            const uint32_t f0 = wd & kI4Lo, f1 = wd & kI4Hi, f2 = w8 & kI4Lo, f3 = w8 & kI4Hi;
             float d[4];
-            mma_f16_c(d, qa[2 * j], wd & kI4Lo, wd & kI4Hi, c0);
-            mma_f16_c(d, qa[2 * j + 1], w8 & kI4Lo, w8 & kI4Hi, d);
+            mma_f16_c(d, qa[2 * j], f0, f1, zero);
+            mma_f16_c(d, qa[2 * j + 1], f2, f3, d);
+            if (j < 2) {
+              uint32_t rest[4];
+              lds128(rest0 + 1024 * j, rest);
+              mma_f16_c(d, rest, f0, f1, d);
+              lds128(rest0 + 1024 * j + 512, rest);
+              mma_f16_c(d, rest, f2, f3, d);
+            }
             const float2 sA = f32x2_of_f16x2(kh[j >> 1]), sB = f32x2_of_f16x2(kh[3 + (j >> 1)]);
-            const uint64_t sc = (j & 1) ? pack_f32x2(sA.y, sB.y) : pack_f32x2(sA.x, sB.x);
-            s01 = fma_f32x2(pack_f32x2(d[0], d[1]), sc, s01);
-            s23 = fma_f32x2(pack_f32x2(d[2], d[3]), sc, s23);
+            const float s0 = (j & 1) ? sA.y : sA.x, s1 = (j & 1) ? sB.y : sB.x;
+            S[nb][0] = fmaf(d[0], s0, S[nb][0]);
+            S[nb][1] = fmaf(d[1], s1, S[nb][1]);
+            S[nb][2] = fmaf(d[2], s0, S[nb][2]);
+            S[nb][3] = fmaf(d[3], s1, S[nb][3]);
           }
-          S[nb][0] = lo_f32(s01);
-          S[nb][1] = hi_f32(s01);
-          S[nb][2] = lo_f32(s23);
-          S[nb][3] = hi_f32(s23);
         }
         // ---- value scales of keys 2 q4, 2 q4 + 1 of each 8: [group] fp16 pairs (even, odd key)
         uint32_t vs[4][kI4VGroups];
@@ -457,7 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
           l_r[0] *= al0;
           l_r[1] *= al1;
 #pragma unroll
-          for (int u = 0; u < kI4VGroups; ++u) {
+          for (int u = 0; u < kI4VGroups; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               o[u][e][0] *= al0;
@@ -465,9 +463,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
               o[u][e][2] *= al1;
               o[u][e][3] *= al1;
             }
-            T[u][0] *= al0;
-            T[u][2] *= al1;
-          }
+          T[0] *= al0;
+          T[1] *= al0;
+          T[2] *= al1;
+          T[3] *= al1;
         }
         const float mu0 = m_r[0] == -INFINITY ? 0.f : m_r[0] - kPBias, mu1 = m_r[1] == -INFINITY ? 0.f : m_r[1] - kPBias;
         uint32_t P[4][2];  // (p of the even key, -p of the odd key) of rows r0, r0 + 8
@@ -477,8 +476,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
           const float b0 = ex2(fmaf(S[nb][2], c_log2, -mu1)), b1 = ex2(fmaf(S[nb][3], c_log2, -mu1));
           l_r[0] += a0 + a1;
           l_r[1] += b0 + b1;
-          P[nb][0] = pack2_f16(a0, -a1);
-          P[nb][1] = pack2_f16(b0, -b1);
+          P[nb][0] = f16x2_of(a0, -a1);
+          P[nb][1] = f16x2_of(b0, -b1);
         }
         // ---- O += P V, 16 keys at a time
 #pragma unroll
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
               mma_f16_c(o[u][2], pa, (y0 & kI4Lo) ^ cl, (y1 & kI4Lo) ^ cl, o[u][2]);
               mma_f16_c(o[u][3], pa, (y0 & kI4Hi) ^ ch, (y1 & kI4Hi) ^ ch, o[u][3]);
               // p (n - 8) = p n - 8 p for the even key, -p (15 - n) + 7 p for the odd one
-              mma_f16_c(T[u], pa, 0xC700C800u, 0xC700C800u, T[u]);
+              mma_f16_c(T, pa, tb[u], tb[u], T);
             }
           }
         }
@@ -522,13 +521,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     if (!ok) break;
 
     // ---- the segment's rows
+    float t_off[2][kI4VGroups];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
+      // columns 0..3 are in lanes 0 and 1 of the quad
+#pragma unroll
+      for (int u = 0; u < kI4VGroups; ++u) t_off[hf][u] = __shfl_sync(0xffffffffu, T[2 * hf + (u & 1)], (lane & ~3) + (u >> 1));
       l_r[hf] += __shfl_xor_sync(0xffffffffu, l_r[hf], 1);
       l_r[hf] += __shfl_xor_sync(0xffffffffu, l_r[hf], 2);
     }
     const bool direct = t_first == 0 && c.t == c.nt;
-    const long piece = 2L * w + (x - (c.t - t_first) > a ? 1 : 0);  // this worker's first or last segment
+    const long piece = 2L * w + (x > c.t - t_first ? 1 : 0);  // this worker's first or last segment
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       if (draft[hf] >= p.q_len) continue;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
           L2 = L * f + ex2(sl - M2);
         }
         sc = p.v_scale * f / L2;
-        if (p.lse && q4 == 0) p.lse[qrow * kHq + h] = (M2 + __log2f(L2)) * kLn2;
+        if (p.lse && q4 == 0) p.lse[qrow * kHq + h] = (M2 + log2f(L2)) * kLn2;
       } else if (q4 == 0) {
         *reinterpret_cast<float2*>(p.ws_ml + (piece * rows + rr) * 2) = make_float2(M, L);
       }
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
         float f[8];  // dims 32 u + 8 q4 + i
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          f[i] = fmaf(o[u][i & 3][2 * hf + (i >> 2)], (i & 1) ? 0x1p20f : 0x1p24f, T[u][2 * hf]) * sc;
+          f[i] = fmaf(o[u][i & 3][2 * hf + (i >> 2)], (i & 1) ? 0x1p20f : 0x1p24f, t_off[hf][u]) * sc;
         if (direct) {
           *reinterpret_cast<uint4*>(p.out + (qrow * kHq + h) * kDv + 32 * u + 8 * q4) =
               make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
@@ -569,16 +572,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
   if (!ok) drain();
 }
 
-// One warp per (query row, head): merges the pieces that share the row's unit, in their order.
-__global__ void __launch_bounds__(256) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
-  const int wid = int((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  if (wid >= p.batch * p.q_len * kHq) return;
-  const int qrow = wid / kHq, h = wid % kHq, s = qrow / p.q_len, g = h / p.group;
+// One block per (query row, head): merges the pieces that share the row's unit.  A long context
+// of a small batch has hundreds, each a dependent load away: the warps take every fourth, and
+// the first warp adds up the warps' sums (a fixed order, whatever the timing).
+__global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
+  __shared__ float4 part[kCombineWarps][32];
+  __shared__ float part_m[kCombineWarps], part_l[kCombineWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qrow = blockIdx.x / kHq, h = blockIdx.x % kHq, s = qrow / p.q_len, g = h / p.group;
   const long long total = p.ws_tbl[p.batch] * p.hkv;
   const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
   if (nt == 0) return;
   const long long u0 = p.ws_tbl[s] * p.hkv + g * nt;
-  const int W = workers_of(p, total);
+  const int W = pieces_of(total, p.min_tiles, p.workers);
   const int w0 = int(((u0 + 1) * W - 1) / total), w1 = int(((u0 + nt) * W - 1) / total);
   if (w0 == w1) return;  // one piece holds the unit: its rows are written
   const int rows = p.n_blocks * 16, rr = (qrow - s * p.q_len) * p.group + h % p.group;
@@ -587,9 +593,13 @@ __global__ void __launch_bounds__(256) decode4_combine_kernel(const __grid_const
   auto piece = [&](int i) { return (i == 0 ? first : 2L * (w0 + i)) * rows + rr; };
   const int n = w1 - w0 + 1;
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
+  for (int i = threadIdx.x; i < n; i += kCombineWarps * 32) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if (lane == 0) part_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) M = fmaxf(M, part_m[i]);
   float sl = -INFINITY;
   if (p.sink) {
     sl = p.sink[h] * kLog2e;
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(256) decode4_combine_kernel(const __grid_const
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
+  for (int i = warp; i < n; i += kCombineWarps) {
     const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * piece(i));
     const float f = ex2(ml.x - M);
     const float4 v = *reinterpret_cast<const float4*>(p.ws_o + piece(i) * kDv + lane * 4);
@@ -608,23 +618,43 @@ __global__ void __launch_bounds__(256) decode4_combine_kernel(const __grid_const
     acc.z += f * v.z;
     acc.w += f * v.w;
   }
+  part[warp][lane] = acc;
+  if (lane == 0) part_l[warp] = L;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int i = 1; i < kCombineWarps; ++i) {
+    const float4 v = part[i][lane];
+    L += part_l[i];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
   if (p.sink) L += ex2(sl - M);
   const float sc = p.v_scale / L;
   *reinterpret_cast<uint2*>(p.out + (long(qrow) * kHq + h) * kDv + lane * 4) =
       make_uint2(pack2_bf16(acc.x * sc, acc.y * sc), pack2_bf16(acc.z * sc, acc.w * sc));
-  if (p.lse && lane == 0) p.lse[long(qrow) * kHq + h] = (M + __log2f(L)) * kLn2;
+  if (p.lse && lane == 0) p.lse[long(qrow) * kHq + h] = (M + log2f(L)) * kLn2;
 }
 
 Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms) {
   Decode4Plan d;
+  // One token over pages: the tensor-core kernel (measured, us per call in graph replay, it against
+  // this file's: 64 sequences of 4096..65536 keys 517 / 548, one of 131001 47 / 64, one of 500
+  // 14.4 / 18.5, 48 of 300..8191 86 / 80).  A ring's unit is two of its tiles, the second mostly
+  // empty, and every unit refills its pipeline: 64 rings of 144 slots 22.7 / 20.6.
+  const bool one = q_len == 1 && !ring;
+  d.tile = one ? kI4TcTile : kI4Tile;
   d.n_blocks = (q_len * (kHq / hkv) + 15) / 16;
   d.nc = d.n_blocks;
-  d.groups = kWarps / d.nc;
+  d.groups = one ? kI4TcGroups : kWarps / d.nc;
   d.stages = kAllStages / d.groups;
-  const int tiles = (unit_keys + kTile - 1) / kTile + 1;  // a window may begin inside a tile
-  // A unit of up to 8 tiles stays whole: a second kernel would cost more than it saves.
-  d.whole_units = ring || tiles <= 9;
-  d.min_tiles = 4;
+  const int tiles = (unit_keys + d.tile - 1) / d.tile + 1;  // a window may begin inside a tile
+  // A unit of up to 256 keys stays whole: a second kernel would cost more than it saves.
+  d.one = one;
+  d.whole_units = ring || unit_keys <= 256;
+  d.min_tiles = one ? 1 : 4;
   const long long units = (long long)batch * hkv;
   const long long most = d.whole_units ? units : (units * tiles + d.min_tiles - 1) / d.min_tiles;
   d.workers = int(most < (long long)sms * d.groups ? most : (long long)sms * d.groups);
@@ -634,14 +664,18 @@ Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end) {
   cudaError_t e;
   if (ev_begin && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_begin), s)) != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(decode4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (p.one) {
+    e = launch_decode4_tc(p, sms, s);
+  } else {
+    e = cudaFuncSetAttribute(decode4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    decode4_kernel<<<p.workers < sms ? p.workers : sms, kWarps * 32, kSmem, s>>>(p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
-  decode4_kernel<<<p.workers < sms ? p.workers : sms, kWarps * 32, kSmem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (ev_end && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_end), s)) != cudaSuccess) return e;
   if (p.whole_units) return cudaSuccess;
-  const long warps = long(p.batch) * p.q_len * kHq;
-  decode4_combine_kernel<<<unsigned((warps * 32 + 255) / 256), 256, 0, s>>>(p);
+  decode4_combine_kernel<<<unsigned(p.batch * p.q_len * kHq), kCombineWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -74,12 +74,15 @@ struct DecodeParams {
 };
 
 // Decode over a 4-bit cache (decode_int4.cu).
-constexpr int kI4Tile = 32;        // keys per tile
-constexpr int kI4MaxBatch = 1024;  // sequences per launch (a prefix table in shared memory)
+constexpr int kI4Tile = 32;        // keys per tile of the draft kernel
+constexpr int kI4TcTile = 128;     // and of the one-token kernel
+constexpr int kI4TcGroups = 2;     // workers per CTA there
+constexpr int kMaxTableBatch = 1024;  // sequences per launch (a prefix table in shared memory)
 struct Decode4Params {
-  CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, 32, 1}
+  CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, tile, 1}
   int batch, hkv, group, q_len, n_blocks;
-  int nc, groups, stages;      // warps per worker (one per row block), workers per CTA, stages per worker
+  int one;                     // the one-token kernel
+  int nc, groups, stages;      // draft kernel: warps per worker (one per row block), workers per CTA, stages per worker
   int workers, min_tiles;      // workers at most; tiles a worker takes at least
   int whole_units;             // pieces hold whole (sequence, KV head) units: no combine
   int window, max_seq_len;
@@ -103,7 +106,8 @@ struct Decode4Params {
   unsigned* status;
 };
 struct Decode4Plan {
-  int n_blocks, nc, groups, stages, workers, min_tiles, whole_units;
+  int one;  // the one-token kernel
+  int tile, n_blocks, nc, groups, stages, workers, min_tiles, whole_units;
 };
 
 // Attention weights per cached slot (weights.cu).
@@ -239,6 +243,7 @@ cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t s);
 void decode_rows(int q_len, int group, int* n_blocks, int* nc, int* n_rp);
 // unit_keys: keys a (sequence, KV head) covers at most
 Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms);
+cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s);
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t s);

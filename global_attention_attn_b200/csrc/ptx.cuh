@@ -178,6 +178,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
          (uint64_t((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The same with the 32-byte swizzle: rows of 32 bytes, 8-row groups `sbo` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t sbo) {
+  return uint64_t((saddr >> 4) & 0x3FFF) | (uint64_t(1) << 16) | (uint64_t((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) |
+         (6ull << 61);
+}
+
 // TMEM loads / stores, shape 32x32b: thread i of the warp reads lane (base + i),
 // consecutive 32-bit columns.
 #define MIMO_TMEM_LD16(taddr, r)                                                                             \

@@ -3,9 +3,9 @@
 #pragma once
 #include <cstdint>
 
-namespace mimo {
+#include "internal.h"
 
-constexpr int kTableMaxBatch = 1024;  // sequences per launch (the prefix table's room)
+namespace mimo {
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -30,6 +30,12 @@ __device__ __forceinline__ void tile_table(long long* tbl, int batch, int lane, 
     carry += __shfl_sync(0xffffffffu, n, 31);
   }
   __syncwarp();
+}
+
+// Pieces that a line of `total` tiles is cut into: piece w is tiles w total / W .. (w + 1) total / W.
+__device__ __forceinline__ int pieces_of(long long total, int min_tiles, int workers) {
+  const long long w = (total + min_tiles - 1) / min_tiles;
+  return int(w < workers ? w : workers);
 }
 
 // A position on the line: sequence s's heads hold hkv * (tbl[s + 1] - tbl[s]) tiles.

@@ -420,7 +420,7 @@ template <int FMT>
 int smem_of(int warps, int q_len, int hkv) {
   const int G = kHq / hkv;
   return 1024 + warps * kStages * Fmt<FMT>::kStage + q_len * (Fmt<FMT>::kSteps * 512 + kHalf * 8 + G * 4 + (FMT == MIMO_DTYPE_INT4 ? G * 32 : 0)) +
-         kMaxWarps * kStages * 8 + 16 + (kTableMaxBatch + 1) * 8;
+         kMaxWarps * kStages * 8 + 16 + (kMaxTableBatch + 1) * 8;
 }
 template <int FMT, int NB>
 cudaError_t launch_weights_fmt(const WeightsParams& p, int sms, cudaStream_t s) {
