@@ -13,173 +13,259 @@ namespace mimo {
 
 namespace {
 
-// Scores as unsigned keys of the same order: -0 equals 0, NaN counts as -infinity.
+// Scores as unsigned keys of the same order, from 0x007FFFFF (-infinity) to 0xFF800000: -0 equals
+// 0, NaN counts as -infinity.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) x = -INFINITY;
   const uint32_t b = __float_as_uint(x + 0.f);
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+constexpr uint32_t kZeroKey = 0x80000000u, kKeepKey = 0xFFFFFFFFu;
+
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;  // 11, 11 and 10 bits a pass
+static_assert(kBins == 4 * kSelThreads, "a thread's bins are one 16-byte read");
+
+// Sum over the warps before this one, and over all, of one value per warp (a block-wide call).
+__device__ __forceinline__ uint2 warps_before(uint32_t* buf, uint32_t mine, int warp, int lane) {
+  if (lane == 0) buf[warp] = mine;
+  __syncthreads();
+  const uint32_t v = lane < kSelWarps ? buf[lane] : 0u;
+  uint32_t incl = v;
+#pragma unroll
+  for (int d = 1; d < kSelWarps; d <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += u;
+  }
+  return make_uint2(__shfl_sync(0xffffffffu, incl - v, warp), __shfl_sync(0xffffffffu, incl, kSelWarps - 1));
+}
 
 }  // namespace
 
-// One cluster per (sequence, KV head) row.  The row is read once (4 bytes a slot, the floor) into
-// the shared memory of the cluster's 1..8 CTAs; the need-th largest score is found by three
-// histogram passes over it (bins summed over the cluster through distributed shared memory,
-// every CTA drawing the same conclusion), then each CTA writes its part of the kept slots at the
-// place that the counts of the parts before it give: ascending, equal scores lowest slot first.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ uint32_t keys[];  // this CTA's part of the row
-  __shared__ __align__(16) uint32_t hist[kBins];
-  __shared__ uint32_t warp_sum[kSelWarps + 1];
-  __shared__ uint32_t found[2];               // bin and how many of it are wanted
-  __shared__ uint32_t w_more[kSelWarps + 1], w_tie[kSelWarps + 1];
-  __shared__ uint32_t part[2];                // this CTA's counts, for the CTAs behind it
+// One cluster per (sequence, KV head) row.  The row is read once (4 bytes a slot, the floor) by the
+// cluster's 1..8 CTAs, and stays with them: 4 Q keys a thread in registers, or in shared memory
+// for the longest rows.  A lane takes 4 neighbouring slots at a step, a warp 128, so that order
+// costs one scan per 128 slots.  The border is found by up to three histogram passes (bins
+// summed over the cluster through distributed shared memory, every CTA drawing the same
+// conclusion; a pass whose bin is wanted whole is the last), then each CTA writes its part of
+// the kept slots at the place that the counts of the parts before it give: ascending, equal
+// scores lowest slot first.  Slots never attended all score 0, so zeros are counted aside and
+// enter the histogram once per warp; other equal scores add up one by one.
+template <int Q>  // steps a warp holds in registers; 0: in shared memory
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ uint4 row_keys[];  // Q == 0: this CTA's part of the row
+  __shared__ __align__(16) uint32_t hist[3][kBins];
+  __shared__ uint32_t sums[2][kSelWarps];
+  __shared__ uint32_t found[3][3];  // of a pass: the border's bin, how many of it are wanted, how many it holds
+  __shared__ uint32_t part[2];      // this CTA's counts, for the CTAs behind it
   cg::cluster_group cl = cg::this_cluster();
   const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+  auto sync = [&]() {
+    if (C == 1) __syncthreads();
+    else cl.sync();
+  };
   const int row = blockIdx.x / C, s = row / p.hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int L = p.seq_lens[s];
   if (L < 0 || L > p.max_seq_len) {
     if (rank == 0 && tid == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
     L = max(0, min(L, p.max_seq_len));
   }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) reinterpret_cast<uint4*>(hist[i])[tid] = make_uint4(0, 0, 0, 0);
   const float* const src = p.scores + long(row) * p.score_stride;
-  const int per = ((L + C - 1) / C + 31) & ~31;  // slots of a CTA
-  const int lo = min(L, rank * per), n = min(L, lo + per) - lo;
-  // the slots that stay whatever their score; all of a row that fits
+  const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  const int per = ((L + C - 1) / C + 127) & ~127;  // slots of a CTA
+  const int lo = min(L, rank * per), end = min(L, lo + per);
+  // a warp's contiguous range of slots, 128 at a step
+  const int range = (((end - lo) + kSelWarps - 1) / kSelWarps + 127) & ~127, steps = range / 128;
+  const int at0 = lo + warp * range + 4 * lane, at_end = min(end, lo + (warp + 1) * range);
+  // Keys: of a slot that stays whatever its score (the first, the recent; every slot of a row that
+  // fits) the largest there is, above any score's; where there is no slot 0, below any score's.
   const bool all = L <= p.keep;
-  const int first = all ? L : p.first, tail = all ? L : L - p.recent;  // candidates: [first, tail)
-  int need = all ? 0 : p.keep - p.first - p.recent;
-  for (int i = tid; i < n; i += kSelThreads) keys[i] = order_key(src[lo + i]);
-  uint32_t prefix = 0, mask = 0;  // keys & mask == prefix are still in question
-  const bool search = need > 0;   // (cluster-uniform: need and L are the row's)
-  if (search) {
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {
-        const int i = i0 + lane, slot = lo + i;
-        const bool in = i < n && slot >= first && slot < tail && (keys[i] & mask) == prefix;
-        const uint32_t who = __ballot_sync(0xffffffffu, in);
-        if (in) {
-          const uint32_t bin = (keys[i] >> shift) & ((1u << bits) - 1);
-          // equal bins of a warp (unattended slots all score 0) are added once
-          const uint32_t same = __match_any_sync(who, bin);
-          if (lane == __ffs(same) - 1) atomicAdd(&hist[bin], uint32_t(__popc(same)));
-        }
-      }
-      cl.sync();
-      // bins from the largest down, 4 a thread, summed over the cluster
-      uint32_t h[4], sum = 0;
+  const int first = all ? L : p.first, tail = all ? L : L - p.recent;
+  uint32_t zeros = 0;
+  auto load = [&](int k) {
+    const int at = at0 + 128 * k;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (wide && at + 4 <= at_end) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + at));
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = 0;
-      for (int r = 0; r < C; ++r) {
-        const uint4 v = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, r) + kBins - 4 - 4 * tid);
-        h[0] += v.w;
-        h[1] += v.z;
-        h[2] += v.y;
-        h[3] += v.x;
-      }
-      sum = h[0] + h[1] + h[2] + h[3];
-      uint32_t incl = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += u;
-      }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - sum;
-      for (int w = 0; w < warp; ++w) before += warp_sum[w];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (before < uint32_t(need) && before + h[e] >= uint32_t(need)) {
-          found[0] = uint32_t(kBins - 1 - 4 * tid - e);
-          found[1] = uint32_t(need) - before;
-        }
-        before += h[e];
-      }
-      cl.sync();  // every CTA has read the bins before they are cleared
-      prefix |= found[0] << shift;
-      mask |= ((1u << bits) - 1) << shift;
-      need = int(found[1]);
+      for (int e = 0; e < 4; ++e)
+        if (at + e < at_end) x[e] = __ldg(src + at + e);
     }
-  }
-  __syncthreads();
-  // prefix: the smallest score kept; need: how many of those that equal it, the first ones
-  auto kind = [&](int i) {  // 2: stays, 1: equals the border, 0: goes
-    const int slot = lo + i;
-    if (slot < first || slot >= tail) return 2;
-    if (!search) return 0;
-    return keys[i] > prefix ? 2 : (keys[i] == prefix ? 1 : 0);
+    uint32_t key[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) key[e] = order_key(x[e]);
+    if (at < first || at + 4 > tail) {  // (tail <= L: the end of the row is in here)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) key[e] = at + e >= at_end ? 0u : (at + e < first || at + e >= tail ? kKeepKey : key[e]);
+    } else if (at + 4 > at_end) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) key[e] = at + e >= at_end ? 0u : key[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) zeros += key[e] == kZeroKey;
+    return make_uint4(key[0], key[1], key[2], key[3]);
   };
-  // a warp's contiguous range
-  const int range = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int i_lo = min(n, warp * range), i_hi = min(n, i_lo + range);
-  uint32_t more = 0, tie = 0;
-  for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
-    const int k = i0 + lane < i_hi ? kind(i0 + lane) : 0;
-    more += __popc(__ballot_sync(0xffffffffu, k == 2));
-    tie += __popc(__ballot_sync(0xffffffffu, k == 1));
+  uint4 reg[Q ? Q : 1];
+  if constexpr (Q > 0) {
+#pragma unroll
+    for (int k = 0; k < Q; ++k) reg[k] = k < steps ? load(k) : make_uint4(0, 0, 0, 0);
+  } else {
+    for (int k = 0; k < steps; ++k) row_keys[(warp * range >> 2) + 32 * k + lane] = load(k);
   }
-  if (lane == 0) {
-    w_more[warp] = more;
-    w_tie[warp] = tie;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t m = 0, t = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      m += w_more[w];
-      t += w_tie[w];
+  zeros = __reduce_add_sync(0xffffffffu, zeros);
+  // f(step, 4 keys) for every 128 slots of this warp, in order
+  auto each = [&](auto&& f) {
+    if constexpr (Q > 0) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k)
+        if (k < steps) {
+          const uint32_t key[4] = {reg[k].x, reg[k].y, reg[k].z, reg[k].w};
+          f(k, key);
+        }
+    } else {
+      for (int k = 0; k < steps; ++k) {
+        const uint4 v = row_keys[(warp * range >> 2) + 32 * k + lane];
+        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+        f(k, key);
+      }
     }
-    part[0] = m;
-    part[1] = t;
+  };
+  int need = p.keep;
+  uint32_t prefix = 0, mask = 0;  // keys & mask == prefix are still in question
+  bool whole = all;               // every slot whose key matches the prefix stays
+  __syncthreads();
+  for (int pass = 0; !whole && pass < 3; ++pass) {  // (cluster-uniform: all of this is the row's)
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+    uint32_t* const hs = hist[pass];
+    const uint32_t low = (1u << bits) - 1;
+    each([&](int, const uint32_t* key) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((key[e] & mask) == prefix && key[e] != kZeroKey) atomicAdd(hs + ((key[e] >> shift) & low), 1u);
+    });
+    if (lane == 0 && zeros && (kZeroKey & mask) == prefix) atomicAdd(hs + ((kZeroKey >> shift) & low), zeros);
+    sync();
+    // bins from the largest down, 4 a thread, summed over the cluster
+    uint32_t h[4] = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int r = 0; r < C; ++r) {
+      const uint4 v = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hs, r) + kBins - 4 - 4 * tid);
+      h[0] += v.w;
+      h[1] += v.z;
+      h[2] += v.y;
+      h[3] += v.x;
+    }
+    const uint32_t sum = h[0] + h[1] + h[2] + h[3];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += u;
+    }
+    uint32_t before = incl - sum + warps_before(sums[pass & 1], __shfl_sync(0xffffffffu, incl, 31), warp, lane).x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (before < uint32_t(need) && before + h[e] >= uint32_t(need)) {
+        found[pass][0] = uint32_t(kBins - 1 - 4 * tid - e);
+        found[pass][1] = uint32_t(need) - before;
+        found[pass][2] = h[e];
+      }
+      before += h[e];
+    }
+    __syncthreads();
+    prefix |= found[pass][0] << shift;
+    mask |= low << shift;
+    need = int(found[pass][1]);
+    whole = found[pass][2] == found[pass][1];
   }
-  cl.sync();
-  more = tie = 0;
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* q = cl.map_shared_rank(part, r);
-    more += q[0];
-    tie += q[1];
-  }
-  for (int w = 0; w < warp; ++w) {
-    more += w_more[w];
-    tie += w_tie[w];
+  // What is above the prefix stays, and of the slots whose key matches it the first `take` (of a row
+  // that fits: all that is above 0)
+  if (all) mask = 0xFFFFFFFFu;
+  const uint32_t take = all ? 0 : uint32_t(need);
+  uint32_t more = 0, tie = 0;
+  each([&](int, const uint32_t* key) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      more += (key[e] & mask) > prefix;
+      tie += (key[e] & mask) == prefix;
+    }
+  });
+  more = __reduce_add_sync(0xffffffffu, more);
+  tie = __reduce_add_sync(0xffffffffu, tie);
+  __syncthreads();  // (the last pass's sums are read)
+  const uint2 m = warps_before(sums[0], more, warp, lane), t = warps_before(sums[1], tie, warp, lane);
+  more = m.x;
+  tie = t.x;
+  if (C > 1) {
+    if (tid == 0) {
+      part[0] = m.y;
+      part[1] = t.y;
+    }
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      const uint32_t* q = cl.map_shared_rank(part, r);
+      more += q[0];
+      tie += q[1];
+    }
   }
   int32_t* const idx = p.idx + long(row) * p.keep;
   float* const out = p.scores_out ? p.scores_out + long(row) * p.keep : nullptr;
-  const uint32_t below = (1u << lane) - 1;
-  for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
-    const int k = i0 + lane < i_hi ? kind(i0 + lane) : 0;
-    const uint32_t bm = __ballot_sync(0xffffffffu, k == 2), bt = __ballot_sync(0xffffffffu, k == 1);
-    const uint32_t t = tie + __popc(bt & below);
-    if (k == 2 || (k == 1 && t < uint32_t(need))) {
-      const uint32_t j = more + __popc(bm & below) + min(t, uint32_t(need));
-      idx[j] = lo + i0 + lane;
-      if (out) out[j] = src[lo + i0 + lane];
+  each([&](int k, const uint32_t* key) {
+    // both counts of the lane's four, scanned over the warp in one word (each at most 128)
+    uint32_t mine = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine += ((key[e] & mask) > prefix ? 1u : 0u) + ((key[e] & mask) == prefix ? 0x10000u : 0u);
+    if (!__any_sync(0xffffffffu, mine)) return;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += u;
     }
-    more += __popc(bm);
-    tie += __popc(bt);
-  }
+    uint32_t mo = more + ((incl - mine) & 0xFFFFu), ti = tie + ((incl - mine) >> 16);
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool up = (key[e] & mask) > prefix, eq = (key[e] & mask) == prefix;
+        if (up || (eq && ti < take)) {
+          const uint32_t j = mo + min(ti, take);
+          const int slot = at0 + 128 * k + e;
+          idx[j] = slot;
+          if (out) out[j] = __ldg(src + slot);
+        }
+        mo += up;
+        ti += eq;
+      }
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
+    more += total & 0xFFFFu;
+    tie += total >> 16;
+  });
   const int count = min(L, p.keep);
   for (int j = count + rank * kSelThreads + tid; j < p.keep; j += C * kSelThreads) {
     idx[j] = -1;
     if (out) out[j] = 0.f;
   }
   if (rank == 0 && tid == 0 && row % p.hkv == 0) p.counts[s] = count;
-  cl.sync();  // no CTA leaves while another reads its counts
+  if (C > 1) cl.sync();  // no CTA leaves while another reads its bins or counts
 }
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
   int c = 1;  // CTAs per row: 4096 slots each at least, 8 at most
   while (c < 8 && c * 4096 < p.max_seq_len) c *= 2;
-  const size_t bytes = size_t((((p.max_seq_len + c - 1) / c + 31) & ~31)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  const int per = ((p.max_seq_len + c - 1) / c + 127) & ~127;
+  const int steps = (per + 128 * kSelWarps - 1) / (128 * kSelWarps);
+  auto kernel = steps <= 2 ? select_kernel<2> : (steps <= 8 ? select_kernel<8> : select_kernel<0>);
+  const size_t bytes = steps <= 8 ? 0 : size_t(steps) * 128 * kSelWarps * 4;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.num_seqs) * p.hkv * c);
@@ -192,7 +278,7 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 namespace {
