@@ -110,21 +110,13 @@ __device__ __forceinline__ void mma_f16_acc(float* d, const uint32_t* a, uint32_
   mma_f16_c(d, a, b0, b1, d);
 }
 
-// Steps KK .. 11 of a tile's products.  The additions to the operands' addresses are part of the
-// instruction's text: as loop invariants the 12 descriptors would spill.
+// Steps KK .. 11 of a tile's products.
 template <int KK>
 __device__ __forceinline__ void product_steps(uint32_t tmem, uint32_t qd_lo, uint32_t qd_hi) {
   if constexpr (KK < 12) {
     constexpr int row = KK < 4 ? 0 : (KK < 8 ? kQOff1 : kQOff2);
-    constexpr uint32_t idesc = idesc_f32acc(128, KK < 4 ? 32 : 16, 0, 0, 0);
-    asm volatile(
-        "{\n\t.reg .b32 d, a, l;\n\t.reg .b64 q;\n\t.reg .pred p;\n\t"
-        "add.u32 d, %0, %1;\n\tadd.u32 a, %0, %2;\n\tadd.u32 l, %3, %4;\n\tmov.b64 q, {l, %5};\n\t"
-        "setp.eq.u32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [d], [a], q, %6, p;\n\t}" ::"r"(tmem),
-        "n"(kColD + col_of(KK >> 1)), "n"(kColA + 8 * KK), "r"(qd_lo), "n"((row + (KK & 3) * 32) >> 4), "r"(qd_hi),
-        "r"(idesc)
-        : "memory");
+    tc_mma_ts_at<kColD + col_of(KK >> 1), kColA + 8 * KK, ((row + (KK & 3) * 32) >> 4)>(
+        tmem, qd_lo, qd_hi, idesc_f32acc(128, KK < 4 ? 32 : 16, 0, 0, 0));
     product_steps<KK + 1>(tmem, qd_lo, qd_hi);
   }
 }

@@ -114,6 +114,7 @@ struct Decode4Plan {
 struct WeightsParams {
   CUtensorMap tm_k;  // bf16 / E4M3 key rows, box {64, 1, 32}
   int batch, hkv, q_len, max_seq_len;
+  int q_first, q_total;  // 4-bit keys: drafts q_first .. q_first + q_len - 1 of q_total
   float scale_log2;
   const uint16_t* q;
   const float* lse;
@@ -246,6 +247,7 @@ Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring
 cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s);
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s);
+cudaError_t launch_weights_int4(WeightsParams p, int sms, cudaStream_t s);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t s);
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t s);
 cudaError_t launch_rope_k(const RopeKParams& p, cudaStream_t s);

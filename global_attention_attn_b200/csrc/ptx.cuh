@@ -161,6 +161,19 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// D[tmem + DOFF] += A[tmem + AOFF] * B[(lo + BOFF, hi)] with the additions in the instruction's text:
+// written as loop invariants, a dozen operands' addresses spill.
+template <uint32_t DOFF, uint32_t AOFF, uint32_t BOFF>
+__device__ __forceinline__ void tc_mma_ts_at(uint32_t tmem, uint32_t desc_lo, uint32_t desc_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .b32 d, a, l;\n\t.reg .b64 q;\n\t.reg .pred p;\n\t"
+      "add.u32 d, %0, %1;\n\tadd.u32 a, %0, %2;\n\tadd.u32 l, %3, %4;\n\tmov.b64 q, {l, %5};\n\t"
+      "setp.eq.u32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [d], [a], q, %6, p;\n\t}" ::"r"(tmem),
+      "n"(DOFF), "n"(AOFF), "r"(desc_lo), "n"(BOFF), "r"(desc_hi), "r"(idesc)
+      : "memory");
+}
+
 // Instruction descriptor, kind::f16 with fp32 accumulate.  ab_fmt: 1 = bf16 A/B,
 // 0 = fp16 A/B (A and B always share one type).  a_mn / b_mn: 1 = operand is
 // MN-major in shared memory, 0 = K-major.

@@ -3,7 +3,9 @@
 // log-sum-exp is given assigned to slot t.  Their running sum over steps is what eviction by
 // accumulated weight ranks slots by.
 //
-// The keys are read once (384, 192 or 108 bytes per slot and KV head) and 8 bytes of scores:
+// (4-bit keys: weights_int4.cu.)
+//
+// The keys are read once (384 or 192 bytes per slot and KV head) and 8 bytes of scores:
 // no second pass for the normalisation (it is given), no exchange between tiles, no atomics (a
 // score belongs to one lane of one tile).  S^T = K Q^T on mma.sync m16n8k16: 16 keys are the
 // rows, the heads of a KV group the columns (two blocks of 8 on 4-head layers, one on 8-head
@@ -15,7 +17,6 @@
 // its warps take the piece's tiles in turn, each with its own two stages of TMA / bulk copies,
 // and share the unit's query fragments (shared memory, up to 8 drafts).
 #include "common.cuh"
-#include "int4.cuh"
 #include "ptx.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
@@ -28,12 +29,12 @@ constexpr int kTile = 32, kMaxWarps = 8, kStages = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int FMT>
-struct Fmt {  // bytes of a stage: 32 key rows (and, 4-bit, their scales)
-  static constexpr int kRow = FMT == MIMO_DTYPE_BF16 ? 384 : (FMT == MIMO_DTYPE_FP8_E4M3 ? 192 : kI4KSlot);
+struct Fmt {  // bytes of a stage: 32 key rows
+  static constexpr int kRow = FMT == MIMO_DTYPE_BF16 ? 384 : 192;
   static constexpr int kStage = (kTile * kRow + 1023) / 1024 * 1024;
-  // query fragments of a draft: 12 steps, 4 remainder steps of the rotated dims, 4-bit: the offset
-  static constexpr int kSteps = FMT == MIMO_DTYPE_INT4 ? 17 : 16;
 };
+// query fragments of a draft: 12 steps, and 4 of the rotated dims' second terms
+constexpr int kSteps = 16;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -49,8 +50,13 @@ __device__ __forceinline__ void mma_bf16_acc(float* d, const uint32_t* a, uint32
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_acc(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  mma_f16_c(d, a, b0, b1, d);
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float2 f32x2_of(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
 // A fragments of 16 keys for step kk.
 template <int FMT>
@@ -83,16 +89,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
   const uint32_t sbase = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane & 3, r0 = lane >> 2;
   const int warps = blockDim.x >> 5;
-  // stages | query fragments | cos, sin | group sums | lse | barriers | tile table
+  // stages | query fragments | cos, sin | lse | barriers | tile table
   const uint32_t ring0 = sbase + warp * kStages * F::kStage;
   uint32_t at = warps * kStages * F::kStage;
   const uint32_t qf = sbase + at;
   uint4* const qf_p = reinterpret_cast<uint4*>(smem + at);
-  at += p.q_len * F::kSteps * 512;
+  at += p.q_len * kSteps * 512;
   float2* const cs = reinterpret_cast<float2*>(smem + at);
   at += p.q_len * kHalf * 8;
-  float* const sums = reinterpret_cast<float*>(smem + at);
-  at += FMT == MIMO_DTYPE_INT4 ? p.q_len * G * 8 * 4 : 0;
   float* const lse2 = reinterpret_cast<float*>(smem + at);
   at += p.q_len * G * 4;
   const uint32_t bar = sbase + at + warp * kStages * 8;
@@ -149,15 +153,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
     const uint32_t dst = ring0 + ist * F::kStage, br = bar + 8 * ist;
     if (lane == 0) {
       mbar_expect_tx(br, kTile * F::kRow);
-      if constexpr (FMT == MIMO_DTYPE_INT4) {
-        const uint8_t* kb = p.k_cache + (long(page) * p.hkv + ic.g) * (kPage * kI4KSlot);
-        bulk_load(dst, kb + slot * kI4KCodes, kTile * kI4KCodes, br);
-        bulk_load(dst + kTile * kI4KCodes, kb + kPage * kI4KCodes + slot * 2 * kI4KGroups, kTile * 2 * kI4KGroups, br);
-      } else {
-        const int row = page * kPage + slot;
+      const int row = page * kPage + slot;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) tma_load_3d(dst + i * (F::kRow / 3) * kTile, &p.tm_k, br, 64 * i, ic.g, row);
-      }
+      for (int i = 0; i < 3; ++i) tma_load_3d(dst + i * (F::kRow / 3) * kTile, &p.tm_k, br, 64 * i, ic.g, row);
     }
     __syncwarp();
     if (++ist == kStages) ist = 0;
@@ -195,60 +193,29 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
       const float2 t = cs[i * kHalf + (d & (kHalf - 1))];
       return d < kHalf ? v * t.x - w * t.y : v * t.x + w * t.y;
     };
-    if constexpr (FMT == MIMO_DTYPE_INT4) {
-      for (int i = warp; i < p.q_len * G; i += warps) {
-#pragma unroll
-        for (int j = 0; j < kI4KGroups; ++j) {
-          float v = qval(i / G, i % G, kI4Group * j + lane);
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-          if (lane == 0) sums[i * 8 + j] = v;
-        }
-      }
-      __syncthreads();
-    }
     float amax = 0.f;
-    for (int it = warp; it < p.q_len * F::kSteps; it += warps) {
-      const int i = it / F::kSteps, kq = it % F::kSteps;
+    for (int it = warp; it < p.q_len * kSteps; it += warps) {
+      const int i = it / kSteps, kq = it % kSteps;
       uint32_t r[4] = {0, 0, 0, 0};  // (b0, b1) of heads r0, then of heads 8 + r0
       const bool rest = kq >= 12 && kq < 16;
       const int kk = rest ? kq - 12 : kq;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int h = 8 * nb + r0;
-        if (FMT == MIMO_DTYPE_INT4 && kq == 16) {
-          // the offset's product (int4.cuh): scales against -8 * group sums / 128, two fp16 terms
-          if (q4 < 3) {
-            const float c0 = sums[(i * G + h) * 8 + 2 * q4] * -0.0625f, c1 = sums[(i * G + h) * 8 + 2 * q4 + 1] * -0.0625f;
-            r[2 * nb] = pack2_f16(c0, c1);
-            const float2 t = f32x2_of_f16x2(r[2 * nb]);
-            r[2 * nb + 1] = pack2_f16(c0 - t.x, c1 - t.y);
-          }
-          continue;
-        }
 #pragma unroll
         for (int bb = 0; bb < 2; ++bb) {
           float v[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            int d;
-            float u = 1.f;
-            if constexpr (FMT == MIMO_DTYPE_BF16) {
-              d = 16 * kk + 8 * bb + 2 * q4 + e;
-            } else if constexpr (FMT == MIMO_DTYPE_FP8_E4M3) {
-              d = 16 * kk + 4 * q4 + 2 * bb + e;
-            } else {
-              d = 32 * (kk >> 1) + 8 * q4 + 2 * (kk & 1) + bb + 4 * e;
-              u = bb ? 0.25f : 4.f;
-            }
-            v[e] = qval(i, h, d) * u;
+            // (E4M3 keys come out of ldmatrix as 4 consecutive dims a lane)
+            v[e] = qval(i, h, FMT == MIMO_DTYPE_BF16 ? 16 * kk + 8 * bb + 2 * q4 + e : 16 * kk + 4 * q4 + 2 * bb + e);
           }
           if (FMT == MIMO_DTYPE_BF16 && kk >= 4) {
             r[2 * nb + bb] = pack2_bf16(v[0], v[1]);
           } else {
             r[2 * nb + bb] = pack2_f16_sat(v[0], v[1], amax);
             if (rest) {
-              const float2 t = f32x2_of_f16x2(r[2 * nb + bb]);
+              const float2 t = f32x2_of(r[2 * nb + bb]);
               r[2 * nb + bb] = pack2_f16(v[0] - t.x, v[1] - t.y);
             }
           }
@@ -259,7 +226,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
     if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
     __syncthreads();
 
-    const float c_log2 = p.scale_log2 * (FMT == MIMO_DTYPE_FP8_E4M3 ? p.k_dequant[g] : (FMT == MIMO_DTYPE_INT4 ? kI4KeyUnit : 1.f));
+    const float c_log2 = p.scale_log2 * (FMT == MIMO_DTYPE_FP8_E4M3 ? p.k_dequant[g] : 1.f);
     float* const row_out = p.scores + (long(s) * p.hkv + g) * p.score_stride;
     for (; mine < n && ok; mine += warps) {
       const int key0 = (c.t + mine) * kTile;
@@ -278,7 +245,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
       const uint32_t kb = ring0 + st * F::kStage;
       float add[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // keys r0, r0 + 8 of either half
       for (int i = 0; i < p.q_len; ++i) {
-        const uint32_t qi = qf + i * F::kSteps * 512 + lane * 16;
+        const uint32_t qi = qf + i * kSteps * 512 + lane * 16;
         float S[2][NB][4];
         auto q_frag = [&](int kq, uint32_t* r) {
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -286,91 +253,30 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
                        : "r"(qi + kq * 512)
                        : "memory");
         };
-        if constexpr (FMT == MIMO_DTYPE_INT4) {
-          uint32_t r[4];
-          q_frag(16, r);
-          uint32_t sc[2][2][kI4KGroups / 2];  // scales of keys r0 and r0 + 8 of either half
-          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            uint32_t aa[4];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t sa = kb + kTile * kI4KCodes + (16 * m + r0 + 8 * e) * 2 * kI4KGroups;
+          for (int nb = 0; nb < NB; ++nb) S[m][nb][0] = S[m][nb][1] = S[m][nb][2] = S[m][nb][3] = 0.f;
+        constexpr int kPer = FMT == MIMO_DTYPE_BF16 ? 1 : 2;  // steps a key fragment load covers
 #pragma unroll
-              for (int j = 0; j < 3; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc[m][e][j]) : "r"(sa + 4 * j) : "memory");
-              aa[e] = aa[2 + e] = q4 == 0 ? sc[m][e][0] : (q4 == 1 ? sc[m][e][1] : (q4 == 2 ? sc[m][e][2] : 0u));
-            }
+        for (int k2 = 0; k2 < 12; k2 += kPer) {
+          uint32_t ka[2][4 * kPer];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma_f16_c(S[m][nb], aa, r[2 * nb], r[2 * nb + 1], zero);
+          for (int m = 0; m < 2; ++m) key_frag<FMT>(kb, 16 * m, k2, lane, ka[m]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) S[m][nb][e] *= kI4OffsetUnit;
-            }
-          }
+          for (int t = 0; t < kPer; ++t) {
+            const int kk = k2 + t;
+            uint32_t r[4], rr[4];
+            q_frag(kk, r);
+            if (kk < 4) q_frag(12 + kk, rr);
 #pragma unroll
-          for (int j = 0; j < kI4KGroups; ++j) {
-            float d[2][NB][4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              uint32_t rr[4];
-              q_frag(2 * j + t, r);
-              if (j < 2) q_frag(12 + 2 * j + t, rr);
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                uint32_t w0, w1;
-                const uint32_t ka = kb + (16 * m + r0) * kI4KCodes + 24 * q4 + 4 * j;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w0) : "r"(ka) : "memory");
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w1) : "r"(ka + 8 * kI4KCodes) : "memory");
-                const uint32_t y0 = t ? w0 >> 8 : w0, y1 = t ? w1 >> 8 : w1;
-                const uint32_t aa[4] = {y0 & kI4Lo, y1 & kI4Lo, y0 & kI4Hi, y1 & kI4Hi};
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  if (t == 0) mma_f16_c(d[m][nb], aa, r[2 * nb], r[2 * nb + 1], zero);
-                  else mma_f16_acc(d[m][nb], aa, r[2 * nb], r[2 * nb + 1]);
-                  if (j < 2) mma_f16_acc(d[m][nb], aa, rr[2 * nb], rr[2 * nb + 1]);
-                }
-              }
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const float2 t0 = f32x2_of_f16x2(sc[m][0][j >> 1]), t1 = f32x2_of_f16x2(sc[m][1][j >> 1]);
-              const float s0 = (j & 1) ? t0.y : t0.x, s1 = (j & 1) ? t1.y : t1.x;
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                S[m][nb][0] = fmaf(d[m][nb][0], s0, S[m][nb][0]);
-                S[m][nb][1] = fmaf(d[m][nb][1], s0, S[m][nb][1]);
-                S[m][nb][2] = fmaf(d[m][nb][2], s1, S[m][nb][2]);
-                S[m][nb][3] = fmaf(d[m][nb][3], s1, S[m][nb][3]);
+                if (FMT == MIMO_DTYPE_BF16 && kk >= 4) mma_bf16_acc(S[m][nb], ka[m] + 4 * t, r[2 * nb], r[2 * nb + 1]);
+                else mma_f16_acc(S[m][nb], ka[m] + 4 * t, r[2 * nb], r[2 * nb + 1]);
+                if (kk < 4) mma_f16_acc(S[m][nb], ka[m] + 4 * t, rr[2 * nb], rr[2 * nb + 1]);
               }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) S[m][nb][0] = S[m][nb][1] = S[m][nb][2] = S[m][nb][3] = 0.f;
-          constexpr int kPer = FMT == MIMO_DTYPE_BF16 ? 1 : 2;  // steps a key fragment load covers
-#pragma unroll
-          for (int k2 = 0; k2 < 12; k2 += kPer) {
-            uint32_t ka[2][4 * kPer];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) key_frag<FMT>(kb, 16 * m, k2, lane, ka[m]);
-#pragma unroll
-            for (int t = 0; t < kPer; ++t) {
-              const int kk = k2 + t;
-              uint32_t r[4], rr[4];
-              q_frag(kk, r);
-              if (kk < 4) q_frag(12 + kk, rr);
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  if (FMT == MIMO_DTYPE_BF16 && kk >= 4) mma_bf16_acc(S[m][nb], ka[m] + 4 * t, r[2 * nb], r[2 * nb + 1]);
-                  else mma_f16_acc(S[m][nb], ka[m] + 4 * t, r[2 * nb], r[2 * nb + 1]);
-                  if (kk < 4) mma_f16_acc(S[m][nb], ka[m] + 4 * t, rr[2 * nb], rr[2 * nb + 1]);
-                }
-            }
           }
         }
         // heads 8 nb + 2 q4, + 1
@@ -419,7 +325,7 @@ namespace {
 template <int FMT>
 int smem_of(int warps, int q_len, int hkv) {
   const int G = kHq / hkv;
-  return 1024 + warps * kStages * Fmt<FMT>::kStage + q_len * (Fmt<FMT>::kSteps * 512 + kHalf * 8 + G * 4 + (FMT == MIMO_DTYPE_INT4 ? G * 32 : 0)) +
+  return 1024 + warps * kStages * Fmt<FMT>::kStage + q_len * (kSteps * 512 + kHalf * 8 + G * 4) +
          kMaxWarps * kStages * 8 + 16 + (kMaxTableBatch + 1) * 8;
 }
 template <int FMT, int NB>
@@ -441,8 +347,7 @@ cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s) {
     case MIMO_DTYPE_BF16 * 2 + 1: return launch_weights_fmt<MIMO_DTYPE_BF16, 1>(p, sms, s);
     case MIMO_DTYPE_FP8_E4M3 * 2: return launch_weights_fmt<MIMO_DTYPE_FP8_E4M3, 2>(p, sms, s);
     case MIMO_DTYPE_FP8_E4M3 * 2 + 1: return launch_weights_fmt<MIMO_DTYPE_FP8_E4M3, 1>(p, sms, s);
-    case MIMO_DTYPE_INT4 * 2: return launch_weights_fmt<MIMO_DTYPE_INT4, 2>(p, sms, s);
-    default: return launch_weights_fmt<MIMO_DTYPE_INT4, 1>(p, sms, s);
+    default: return launch_weights_int4(p, sms, s);
   }
 }
 
