@@ -282,7 +282,8 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
 }
 
 namespace {
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kMoveSlots = 32;
+static_assert(kPage % kMoveSlots == 0, "a block stays within a page");
 
 __device__ __forceinline__ void widen_e4m3(const uint2& r, float sc, float* x) {
   const uint32_t w[2] = {r.x, r.y};
@@ -295,22 +296,24 @@ __device__ __forceinline__ void widen_e4m3(const uint2& r, float sc, float* x) {
 }
 }  // namespace
 
-// A block moves the slots of one destination page and KV head, bound by the bytes read and
-// written: 16-byte pieces, neighbouring threads on neighbouring pieces of a row, several in
+// A block moves 32 slots of one destination page and KV head (128 left an SM one or two blocks
+// and their latencies at a few thousand slots: 13.8 us for 6750 of 4 heads widened), bound by the
+// bytes read and written: 16-byte pieces, neighbouring threads on neighbouring pieces of a row, several in
 // flight per thread.  SRC is the source's format; WIDE: the destination is bf16 (dims 0..63 of
 // a key fp16), and a thread makes 8 dims of it.
 template <int SRC, bool WIDE>
 __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_constant__ GatherParams p) {
-  __shared__ long from[kPage];  // source entry (page * 128 + slot) of each destination slot, or -1
-  const int s = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * kPage, tid = threadIdx.x;
+  __shared__ long from[kMoveSlots];  // source entry (page * 128 + slot) of each destination slot, or -1
+  const int s = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * kMoveSlots, tid = threadIdx.x;
   int count = p.counts[s];
   if (count > p.max_count) {
     if (g == 0 && blockIdx.x == 0 && tid == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
     count = p.max_count;
   }
-  const int n = min(kPage, count - j0);
+  const int n = min(kMoveSlots, count - j0);
   if (n <= 0) return;
-  const int dst_page = blockIdx.x < p.max_pages_dst ? p.table_dst[long(s) * p.max_pages_dst + blockIdx.x] : -1;
+  const int dst_at = j0 / kPage, slot0 = j0 % kPage;
+  const int dst_page = dst_at < p.max_pages_dst ? p.table_dst[long(s) * p.max_pages_dst + dst_at] : -1;
   if (dst_page < 0 || dst_page >= p.num_pages_dst) {
     if (tid == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
     return;
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_const
   // row `entry` of KV head g of a wide or E4M3 cache, row bytes b; of a 4-bit block: its codes
   auto row_of = [&](auto* base, long entry, int b) { return base + (entry * p.hkv + g) * b; };
   auto block_of = [&](auto* base, long page, int b) { return base + (page * p.hkv + g) * (long(kPage) * b); };
-  const long to0 = long(dst_page) * kPage;
+  const long to0 = long(dst_page) * kPage + slot0;
 
   auto move = [&](const uint8_t* src, uint8_t* dst, int slot_bytes, int code_bytes) {
     // 16-byte pieces of the rows (codes)
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_const
       const long f = from[r];
       if (f < 0) continue;
       const uint8_t* a = kI4 ? block_of(src, f / kPage, slot_bytes) + f % kPage * code_bytes : row_of(src, f, slot_bytes);
-      uint8_t* b = kI4 ? block_of(dst, dst_page, slot_bytes) + r * code_bytes : row_of(dst, to0 + r, slot_bytes);
+      uint8_t* b = kI4 ? block_of(dst, dst_page, slot_bytes) + (slot0 + r) * code_bytes : row_of(dst, to0 + r, slot_bytes);
       reinterpret_cast<uint4*>(b)[c] = __ldg(reinterpret_cast<const uint4*>(a) + c);
     }
     if constexpr (kI4) {  // the rows of scales, 4-byte pieces
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_const
         const long f = from[r];
         if (f < 0) continue;
         const uint8_t* a = block_of(src, f / kPage, slot_bytes) + kPage * code_bytes + f % kPage * sb;
-        uint8_t* b = block_of(dst, dst_page, slot_bytes) + kPage * code_bytes + r * sb;
+        uint8_t* b = block_of(dst, dst_page, slot_bytes) + kPage * code_bytes + (slot0 + r) * sb;
         reinterpret_cast<uint32_t*>(b)[c] = __ldg(reinterpret_cast<const uint32_t*>(a) + c);
       }
     }
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_const
 }
 
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t s) {
-  const dim3 grid((p.max_count + kPage - 1) / kPage, p.hkv, p.num_seqs);
+  const dim3 grid((p.max_count + kMoveSlots - 1) / kMoveSlots, p.hkv, p.num_seqs);
   if (p.out_dtype == p.cache_dtype) {
     if (p.cache_dtype == MIMO_DTYPE_BF16) gather_kernel<MIMO_DTYPE_BF16, false><<<grid, kMoveThreads, 0, s>>>(p);
     else if (p.cache_dtype == MIMO_DTYPE_FP8_E4M3) gather_kernel<MIMO_DTYPE_FP8_E4M3, false><<<grid, kMoveThreads, 0, s>>>(p);
