@@ -10,10 +10,8 @@
 // thread-per-key layout are free of shuffles, and a key's scales are read and converted once.
 //   - The rotated query dims enter as two fp16 terms (no 16-bit type holds them to the digits of
 //     an fp32 log-sum-exp); the code offset is one more k-step, a constant row of A against -8 *
-//     the query's group sums (two fp16 terms).  A tcgen05.mma of 128 rows takes about 56 cycles
-//     for any N up to 64 (77 at 128), so both terms are columns of one product (N = 32) and the
-//     offset is one product over all columns, which also starts the sums: 13 products a tile, not
-//     22.  Tensor memory of a group: 96 columns of keys, 8 of the constant, 128 of sums.
+//     the query's group sums (two fp16 terms).  Both terms are columns of one product (N = 32), and the
+//     offset is one product over all columns, which also starts the sums: 13 products a tile.  Tensor memory of a group: 96 columns of keys, 8 of the constant, 128 of sums.
 //   - O = P V stays on mma.sync with the accumulators in registers (decode_int4.cu explains the
 //     operands): P goes through shared memory, transposed by ldmatrix.  Each warp sums over its
 //     own keys against its own reference; the four warps meet at the end of a unit.
@@ -148,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
   const uint32_t sbase = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool issuer = warp >= kGroups * 4;
-  const int grp = issuer ? warp - kGroups * 4 : warp >> 2, gw = warp & 3;
+  const int grp = __shfl_sync(0xffffffffu, issuer ? warp - kGroups * 4 : warp >> 2, 0), gw = warp & 3;
   const int q4 = lane & 3, r0 = lane >> 2;
   const uint32_t qt = sbase + grp * kQBytes, pt = sbase + kOffP + warp * kPBytes;
   const uint32_t ring0 = sbase + kOffStage + grp * kStages * kStage;
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot + grp * kColGroup;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot + grp * kColGroup, 0);  // (known uniform)
   const uint32_t t_lane = tmem + (uint32_t(gw * 32) << 16);
 
   // ---- this group's piece of the line
@@ -285,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
       for (; copied < n_all && copied < kStages; ++copied) copy(copied);
       for (; done < n_all && ok; ++done) {
         if (!(ok = wait_w(a_ready, done & 1))) break;
-        if (lane == 0) products();
+        if (elect_one()) products();
         __syncwarp();
         // the stage of tile done - 2 is read: its next copy
         if (done >= 2 && copied < n_all) {
@@ -293,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
           copy(copied++);
         }
       }
-      if (!ok && lane == 0) {
+      if (!ok && elect_one()) {
         // a wait ran out: the copies and products under way end before the block does
         int dummy = 0;
         for (int i = copied > kStages ? copied - kStages : 0; i < copied; ++i)

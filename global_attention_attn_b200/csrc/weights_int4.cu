@@ -104,15 +104,15 @@ __device__ __forceinline__ void products(uint32_t tmem, uint64_t qd, uint64_t qo
 
 // Parts PT .. of a tile: each once its keys stand in A and its old sums are read.
 template <int N, int PT, class W>
-__device__ __forceinline__ bool issue_part(int n, W&& ready, int lane, uint32_t tmem, uint64_t qd, uint64_t qo, uint32_t done0) {
+__device__ __forceinline__ bool issue_part(W&& ready, uint32_t tmem, uint64_t qd, uint64_t qo, uint32_t done0) {
   if constexpr (PT < kParts) {
     if (!ready(PT)) return false;
-    if (lane == 0) {
+    if (elect_one()) {
       products<N, PT>(tmem, qd, qo);
       tc_commit(done0 + 8 * PT);
     }
     __syncwarp();
-    return issue_part<N, PT + 1>(n, ready, lane, tmem, qd, qo, done0);
+    return issue_part<N, PT + 1>(ready, tmem, qd, qo, done0);
   }
   return true;
 }
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // (known uniform)
   const long long total = tbl[p.batch] * p.hkv;
   const long long a = blockIdx.x * total / gridDim.x, b = (blockIdx.x + 1) * total / gridDim.x;
   const int n_all = int(b - a);
@@ -207,14 +207,14 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
       bool ok = true;
       for (; copied < n_all && copied < kStages; ++copied) copy(copied);
       for (; n < n_all && ok; ++n) {
-        ok = issue_part<N, 0>(n, [&](int h) { return wait_w(a_ready(h), n & 1); }, lane, tmem, qd, qo, done(0));
+        ok = issue_part<N, 0>([&](int h) { return wait_w(a_ready(h), n & 1); }, tmem, qd, qo, done(0));
         if (!ok) break;
         if (n >= 2 && copied < n_all) {
           if (!(ok = wait_w(empty(copied % kStages), (copied / kStages - 1) & 1))) break;
           copy(copied++);
         }
       }
-      if (!ok && lane == 0) {
+      if (!ok && elect_one()) {
         // a wait ran out: the copies and products under way end before the block does
         int dummy = 0;
         for (int i = copied > kStages ? copied - kStages : 0; i < copied; ++i)
