@@ -249,8 +249,9 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
                                   ring ? ring_slots : decode_unit_keys(a->max_seq_len, a->layer.window, q_len), ring,
                                   d.sms < kI4Sms ? d.sms : kI4Sms);
   while (plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
-  if (!ring && (long(a->num_pages) * hkv > INT_MAX || long(a->max_seq_len) * a->batch / kI4Tile * hkv / plan.workers > INT_MAX / 2))
-    return fail(MIMO_ERR_UNSUPPORTED, "%s: num_pages * num_kv_heads, or the keys of one worker, pass 2^31", fn);
+  const long tiles = a->max_seq_len / kPage + 2L;
+  if (!ring && (long(a->num_pages) * hkv > INT_MAX || tiles * (a->batch < kMaxTableBatch ? a->batch : kMaxTableBatch) * hkv > INT_MAX))
+    return fail(MIMO_ERR_UNSUPPORTED, "%s: num_pages * num_kv_heads, or the pages of max_seq_len in all, pass 2^31", fn);
   {
     const cuuint64_t slots = ring ? ring_slots : kPage;
     const cuuint64_t blocks = cuuint64_t(ring ? a->batch : a->num_pages) * hkv;
@@ -267,7 +268,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   p.group = kHq / hkv;
   p.q_len = q_len;
   p.n_blocks = plan.n_blocks;
-  p.one = plan.one;
+  p.tc = plan.tc;
   p.nc = plan.nc;
   p.groups = plan.groups;
   p.stages = plan.stages;

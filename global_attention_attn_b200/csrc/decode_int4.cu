@@ -640,21 +640,17 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
 
 Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms) {
   Decode4Plan d;
-  // One token over pages: the tensor-core kernel (measured, us per call in graph replay, it against
-  // this file's: 64 sequences of 4096..65536 keys 517 / 548, one of 131001 47 / 64, one of 500
-  // 14.4 / 18.5, 48 of 300..8191 86 / 80).  A ring's unit is two of its tiles, the second mostly
-  // empty, and every unit refills its pipeline: 64 rings of 144 slots 22.7 / 20.6.
-  const bool one = q_len == 1 && !ring;
-  d.tile = one ? kI4TcTile : kI4Tile;
+  const bool tc = !ring;
   d.n_blocks = (q_len * (kHq / hkv) + 15) / 16;
+  d.tile = tc ? kI4TcTile : kI4Tile;
   d.nc = d.n_blocks;
-  d.groups = one ? kI4TcGroups : kWarps / d.nc;
+  d.groups = tc ? (d.n_blocks == 1 ? 2 : 1) : kWarps / d.nc;
   d.stages = kAllStages / d.groups;
   const int tiles = (unit_keys + d.tile - 1) / d.tile + 1;  // a window may begin inside a tile
   // A unit of up to 256 keys stays whole: a second kernel would cost more than it saves.
-  d.one = one;
+  d.tc = tc;
   d.whole_units = ring || unit_keys <= 256;
-  d.min_tiles = one ? 1 : 4;
+  d.min_tiles = tc ? 1 : 4;
   const long long units = (long long)batch * hkv;
   const long long most = d.whole_units ? units : (units * tiles + d.min_tiles - 1) / d.min_tiles;
   d.workers = int(most < (long long)sms * d.groups ? most : (long long)sms * d.groups);
@@ -664,7 +660,7 @@ Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end) {
   cudaError_t e;
   if (ev_begin && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_begin), s)) != cudaSuccess) return e;
-  if (p.one) {
+  if (p.tc) {
     e = launch_decode4_tc(p, sms, s);
   } else {
     e = cudaFuncSetAttribute(decode4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

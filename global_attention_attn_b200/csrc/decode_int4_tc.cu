@@ -1,25 +1,23 @@
-// One-token decode over a 4-bit paged cache, the logits on the 5th-generation tensor cores.
+// Decode and draft verification over a 4-bit paged cache on the 5th-generation tensor cores.
 //
-// The mma.sync kernel of decode_int4.cu spends most of its issue slots on the logits: an
-// mma.sync m16n8k16 takes 8.9 cycles of a scheduler during which the other instructions it
-// dispatches do not come for free (an mma.sync and four LOP3, 2 cycles each, measured 12.2 to
-// 12.8 cycles, not 8.9).  Here S^T = K Q^T runs as tcgen05.mma: a group of four warps takes 128
-// keys, each thread unpacks its own key (int4.cuh: one shift and four ANDs per 8 codes, no
-// conversion) into its row of the A operand in tensor memory, and reads back 16 heads times 6
-// group sums of its row, to which it applies its key's 6 scales.  Both sides of a
-// thread-per-key layout are free of shuffles, and a key's scales are read and converted once.
-//   - The rotated query dims enter as two fp16 terms (no 16-bit type holds them to the digits of
-//     an fp32 log-sum-exp); the code offset is one more k-step, a constant row of A against -8 *
-//     the query's group sums (two fp16 terms).  Both terms are columns of one product (N = 32), and the
-//     offset is one product over all columns, which also starts the sums: 13 products a tile.  Tensor memory of a group: 96 columns of keys, 8 of the constant, 128 of sums.
-//   - O = P V stays on mma.sync with the accumulators in registers (decode_int4.cu explains the
-//     operands): P goes through shared memory, transposed by ldmatrix.  Each warp sums over its
-//     own keys against its own reference; the four warps meet at the end of a unit.
-// The keys of tile i + 1 are unpacked before the softmax and P V of tile i, so the tensor cores
-// work behind the arithmetic.  Two groups per CTA, one CTA per SM, four 23 KB stages each; a
-// ninth and a tenth warp issue the groups' copies and products (by one of the four warps, the
-// other three waited for its 22 issues every tile: 716 against 530 us with them left out), so the
-// warps that compute meet only on mbarriers, and at the ends of units.
+// 180 bytes per (key, KV head), 57 FLOP per byte and draft, and every element unpacked first: on
+// mma.sync (decode_int4.cu) an m16n8k16 takes 8.9 cycles of a scheduler during which the other
+// instructions it dispatches do not come for free (an mma.sync and four LOP3, 2 cycles each,
+// measured 12.2 to 12.8 cycles), and every draft unpacks the tile again.  Here both products are
+// tcgen05.mma, so the warps only unpack and exponentiate, once for all drafts:
+//   - S^T = K Q^T, 128 keys as the rows of A in tensor memory: a thread unpacks half of its own
+//     key's words (int4.cuh: one shift and four ANDs per 8 codes, no conversion) and applies the
+//     key's 6 scales to its half of the columns' 6 group sums.  The rotated query dims enter as
+//     two fp16 terms (no 16-bit type holds them to the digits of an fp32 log-sum-exp); the code
+//     offset is one more k-step, a constant row of A against -8 * the query's group sums.
+//   - O^T = V^T P^T: a thread unpacks half of its key's value row to fp16, scale applied, into
+//     shared memory ([key][dim], the M-major operand), and stores its weights beside it.  The
+//     sums of all tiles stay in tensor memory, 128 dims x columns.
+// A column is a query row of the KV head (draft, head).  Its reference is common to the tile's
+// warps (they share the sums): they meet at one barrier per tile, where a logit that has passed
+// the reference by 2^6 makes all of them move it; else nothing is rescaled.
+// Eight warps (two threads a key) work on a tile, a ninth issues copies and products.  One token of
+// a KV head is 16 columns: its tensor memory allows two such streams per SM, more columns one.
 #include "common.cuh"
 #include "int4.cuh"
 #include "ptx.cuh"
@@ -30,47 +28,52 @@ namespace mimo {
 
 namespace {
 
-constexpr int kTile = kI4TcTile, kGroups = kI4TcGroups, kStages = 4;
-constexpr int kThreads = (kGroups + 1) * 128;  // the groups, and a warpgroup whose first warps issue
-// registers: 384 x 168 at launch = 256 x 224 + 128 x 56
-constexpr int kRegsWork = 224, kRegsIssue = 56;
-static_assert(kGroups * 128 * kRegsWork + 128 * kRegsIssue <= kThreads * 168, "register split");
+constexpr int kTile = kI4TcTile;
 static_assert(kTile == kPage, "a tile is a page");
-// stage: value codes (64-byte swizzle), key codes, key scales, value scales
-constexpr int kOffK = kTile * kI4VCodes, kOffKs = kOffK + kTile * kI4KCodes;
-constexpr int kOffVs = kOffKs + kTile * 2 * kI4KGroups, kStage = kOffVs + kTile * 2 * kI4VGroups;
-static_assert(kStage % 512 == 0, "64-byte swizzle alignment");
-// query operand of a group, 128-byte rows of 64 elements with the 128-byte swizzle: dims 0..63 of
-// 16 heads and their second terms (32 rows), dims 64..127, dims 128..191; then the offsets: a
-// 32-byte row (16 elements, 32-byte swizzle) per column of sums
-constexpr int kQOff1 = 32 * 128, kQOff2 = kQOff1 + 16 * 128, kQOffset = kQOff2 + 16 * 128;
-constexpr int kCols = 128;  // of sums: groups 0, 1: 16 heads and their second terms, groups 2..5: 16 heads
-constexpr int kQBytes = kQOffset + kCols * 32;
-__host__ __device__ constexpr int col_of(int j) { return j < 2 ? 32 * j : 64 + 16 * (j - 2); }
-constexpr int kPRow = 48, kPBytes = 32 * kPRow;  // a warp's P: 16 heads per key, rows apart in banks
-constexpr int kOffP = kGroups * kQBytes;
-constexpr int kOffStage = kOffP + kGroups * 4 * kPBytes;
-static_assert(kOffStage % 512 == 0, "stage alignment");
-constexpr int kOffBar = kOffStage + kGroups * kStages * kStage;
-constexpr int kOffX = kOffBar + 256;  // a group's (reference, sum) of 16 heads per warp
-constexpr int kOffTbl = kOffX + kGroups * 4 * 2 * 16 * 4;
-constexpr int kSmem = kOffTbl + (kMaxTableBatch + 1) * 8 + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
-// tensor memory of a group
-constexpr uint32_t kColA = 0, kColOne = 96, kColD = 128, kColGroup = 256;
-static_assert(kColD + kCols <= kColGroup && kGroups * kColGroup <= 512, "tensor memory");
+// a tile's keys: codes, scales; its values: codes (64-byte swizzle), scales
+constexpr int kKBytes = kTile * kI4KSlot, kOffKs = kTile * kI4KCodes;
+constexpr int kVBytes = kTile * kI4VSlot, kOffVs = kTile * kI4VCodes;
+static_assert(kVBytes % 512 == 0, "64-byte swizzle alignment");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Weights are 2^(z - ref): ref is a row's maximum when it was set, and moves only when a logit
-// passes it by more than this many powers of two (2^6 * 1023, the largest value scale an
-// append stores, is still a finite fp16).
+// Weights are 2^(z - ref): ref is a column's maximum when it was set, and moves only when a logit
+// passes it by more than this many powers of two.
 constexpr float kSlack = 6.f;
 
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
+// What depends on the number of columns.
+template <int N>
+struct Lay {
+  // streams, threads a key, warps and threads of a stream
+  static constexpr int kStreams = N == 16 ? 2 : 1, kT = 4 / kStreams, kW = 4 * kT, kN = 32 * kW;
+  static constexpr int kThreads = kStreams * kN + 128;  // and a warpgroup whose first warps issue
+  // registers at launch, of a thread that computes and of one that issues
+  static constexpr int kRegs = 96, kRegsWork = 104, kRegsIssue = 64;
+  static_assert(kStreams * kN * kRegsWork + 128 * kRegsIssue <= kThreads * kRegs, "register split");
+  // A tile's logits run in parts of kPer groups, in one where their columns all fit (kSep), else the
+  // parts take turns in the same columns.
+  static constexpr bool kSep = 7 * N + 112 <= 512;
+  static constexpr int kPer = kSep ? kI4KGroups : (N <= 96 ? 3 : 2), kParts = kI4KGroups / kPer;
+  static constexpr uint32_t kColA = 0, kColOne = 96, kColD = 112, kColO = kColD + (kSep ? kI4KGroups : kPer) * N;
+  static constexpr uint32_t kColStream = 256;
+  static_assert(kColO + N <= (kStreams == 1 ? 512 : kColStream), "tensor memory");
+  __host__ __device__ static constexpr uint32_t col(int j) { return kColD + (kSep ? j : j % kPer) * N; }
+  // a stream's shared memory: query operand (N rows of 64 elements, 128-byte swizzle: dims 0..63,
+  // 64..127, 128..191, the second terms of 0..63; a 32-byte row of the offset per column of sums),
+  // values, weights, then the rings of copied tiles
+  static constexpr int kQChunk = N * 128, kQOffset = 4 * kQChunk;
+  static constexpr int kOffV = (kQOffset + kI4KGroups * N * 32 + 1023) / 1024 * 1024;
+  static constexpr int kVChunk = kTile * 128, kOffP = kOffV + 2 * kVChunk;
+  static constexpr int kPBytes = N == 16 ? kTile * 32 : (N + 63) / 64 * kVChunk;
+  static constexpr int kStagesK = N <= 64 && N > 16 ? 4 : 3, kStagesV = N <= 64 && N > 16 ? 3 : 2;
+  static constexpr int kOffRingV = kOffP + kPBytes, kOffRingK = kOffRingV + kStagesV * kVBytes;
+  static constexpr int kStream = (kOffRingK + kStagesK * kKBytes + 1023) / 1024 * 1024;
+  // per stream: references, factors, the warps' maxima or sums, cos and sin
+  static constexpr int kOffX = kStreams * kStream, kXBytes = 6 * N * 4 + (N < 64 ? N / 8 : 8) * kHalf * 8;
+  static constexpr int kOffBar = kOffX + kStreams * kXBytes;
+  static constexpr int kOffTbl = kOffBar + 288;
+  static constexpr int kSmem = kOffTbl + (kMaxTableBatch + 1) * 8 + 1024;
+  static_assert(kOffRingV % 512 == 0 && kSmem <= 232448, "shared memory budget");
+};
+
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* r) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -82,21 +85,20 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr) : "memory");
   return a;
 }
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t* r) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t a;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(a) : "r"(addr) : "memory");
+  return a;
+}
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* r) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint16_t v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// (x ^ flip) & mask, one LOP3: an immediate mask and `flip` in a register
-__device__ __forceinline__ uint32_t field(uint32_t x, uint32_t flip, uint32_t mask) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(d) : "r"(x), "r"(flip), "r"(mask));
   return d;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -104,19 +106,60 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ void mma_f16_acc(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  mma_f16_c(d, a, b0, b1, d);
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
+// Registers whose load a wait before has covered.
+template <int C>
+__device__ __forceinline__ void tied(uint32_t* d) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) asm volatile("" : "+r"(d[i]));
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+// (x & mask) | base, one LOP3 (base in a register)
+__device__ __forceinline__ uint32_t field(uint32_t x, uint32_t mask, uint32_t base) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(base));
+  return d;
+}
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
 
-// Steps KK .. 11 of a tile's products.
-template <int KK>
-__device__ __forceinline__ void product_steps(uint32_t tmem, uint32_t qd_lo, uint32_t qd_hi) {
-  if constexpr (KK < 12) {
-    constexpr int row = KK < 4 ? 0 : (KK < 8 ? kQOff1 : kQOff2);
-    tc_mma_ts_at<kColD + col_of(KK >> 1), kColA + 8 * KK, ((row + (KK & 3) * 32) >> 4)>(
-        tmem, qd_lo, qd_hi, idesc_f32acc(128, KK < 4 ? 32 : 16, 0, 0, 0));
-    product_steps<KK + 1>(tmem, qd_lo, qd_hi);
+// Steps KK .. of part PT of a tile's logits (two terms for groups 0, 1).
+template <int N, int PT, int KK>
+__device__ __forceinline__ void logit_steps(uint32_t tmem, uint32_t lo, uint32_t hi) {
+  using Y = Lay<N>;
+  if constexpr (KK < 2 * Y::kPer * (PT + 1)) {
+    constexpr uint32_t idesc = idesc_f32acc(128, N, 0, 0, 0), d = Y::col(KK >> 1), a = Y::kColA + 8 * KK;
+    tc_mma_ts_at<d, a, (((KK >> 2) * Y::kQChunk + (KK & 3) * 32) >> 4)>(tmem, lo, hi, idesc);
+    if constexpr (KK < 4) tc_mma_ts_at<d, a, ((3 * Y::kQChunk + KK * 32) >> 4)>(tmem, lo, hi, idesc);
+    logit_steps<N, PT, KK + 1>(tmem, lo, hi);
   }
+}
+// The offset over columns COL .. of part PT, which starts the sums.
+template <int N, int PT, int COL>
+__device__ __forceinline__ void logit_offset(uint32_t tmem, uint64_t qo) {
+  using Y = Lay<N>;
+  constexpr int all = Y::kPer * N;
+  if constexpr (COL < all) {
+    constexpr int n = all - COL > 240 ? 240 : all - COL;
+    tc_mma_ts(tmem + Y::col(Y::kPer * PT) + COL, tmem + Y::kColOne, qo + (((all * PT + COL) * 32) >> 4),
+              idesc_f32acc(128, n, 0, 0, 0), 0u);
+    logit_offset<N, PT, COL + n>(tmem, qo);
+  }
+}
+template <int N, int PT>
+__device__ __forceinline__ void logits_part(uint32_t tmem, uint64_t qd, uint64_t qo) {
+  logit_offset<N, PT, 0>(tmem, qo);
+  logit_steps<N, PT, 2 * Lay<N>::kPer * PT>(tmem, uint32_t(qd), uint32_t(qd >> 32));
 }
 
 // Keys a sequence's unit covers: [lo, hi], and its first tile and tile count.
@@ -126,8 +169,8 @@ struct Span {
 __device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
   Span u;
   u.hi = min(ctx, p.max_seq_len) - 1;
-  u.lo = p.window > 0 ? max(0, ctx - p.window) : 0;
-  if (ctx < 1 || u.lo > u.hi) {
+  u.lo = p.window > 0 ? max(0, ctx - p.q_len + 1 - p.window) : 0;
+  if (ctx < p.q_len || u.lo > u.hi) {
     u.t0 = u.nt = 0;
   } else {
     u.t0 = u.lo / kTile;
@@ -138,48 +181,58 @@ __device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
 
 }  // namespace
 
-template <int NB>  // blocks of 8 heads per KV head: 2 (global layers) or 1
-__global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_constant__ Decode4Params p) {
-  constexpr int G = 8 * NB, H2 = G / 2;
+template <int N>
+__global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const __grid_constant__ Decode4Params p) {
+  using Y = Lay<N>;
+  constexpr int kT = Y::kT, NC = N / kT, kParts = Y::kParts, kPer = Y::kPer;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool issuer = warp >= kGroups * 4;
-  const int grp = __shfl_sync(0xffffffffu, issuer ? warp - kGroups * 4 : warp >> 2, 0), gw = warp & 3;
-  const int q4 = lane & 3, r0 = lane >> 2;
-  const uint32_t qt = sbase + grp * kQBytes, pt = sbase + kOffP + warp * kPBytes;
-  const uint32_t ring0 = sbase + kOffStage + grp * kStages * kStage;
-  const uint32_t bar0 = sbase + kOffBar + grp * 96;
-  auto full = [&](int i) { return bar0 + 8 * i; };
-  auto empty = [&](int i) { return bar0 + 8 * (kStages + i); };
-  const uint32_t a_ready = bar0 + 16 * kStages;   // a tile's keys stand in A, the sums before them are read
-  const uint32_t mma_done = a_ready + 8;          // its sums stand in D
-  volatile int* const bad_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 192 + grp * 8);  // [2]
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 208);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + 224);
-  float* const xch = reinterpret_cast<float*>(smem + kOffX) + grp * 128;  // [4 warps][ref 16 | sum 16]
-  long long* const tbl = reinterpret_cast<long long*>(smem + kOffTbl);
-  if (!issuer && gw == 0 && lane == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), 4);
+  const bool issuer = warp >= Y::kStreams * Y::kW;
+  const int str = __shfl_sync(0xffffffffu, issuer ? warp - Y::kStreams * Y::kW : warp / Y::kW, 0);
+  const int gq = warp & 3, hw = (warp >> 2) & (kT - 1);  // the quarter of the tile's keys, and which of a key's threads
+  const int tid = threadIdx.x & (Y::kN - 1);                 // within the stream
+  const uint32_t base = sbase + str * Y::kStream;
+  const uint32_t vt = base + Y::kOffV, pt = base + Y::kOffP;
+  const uint32_t ring_k = base + Y::kOffRingK, ring_v = base + Y::kOffRingV;
+  float* const nref = reinterpret_cast<float*>(smem + Y::kOffX + str * Y::kXBytes);  // [N] minus the references
+  float* const fac = nref + N;                                                       // [N] what a move multiplies with
+  float* const wmax = fac + N;                                                       // [4][N]
+  float2* const cs = reinterpret_cast<float2*>(wmax + 4 * N);
+  const uint32_t bar0 = sbase + Y::kOffBar + str * 128;
+  auto full_k = [&](int i) { return bar0 + 8 * i; };
+  auto full_v = [&](int i) { return bar0 + 32 + 8 * i; };
+  auto ready = [&](int h) { return bar0 + 56 + 8 * h; };  // part h of a tile's logits may run
+  auto done = [&](int h) { return bar0 + 80 + 8 * h; };   // its sums stand
+  const uint32_t pv_ready = bar0 + 104, pv_done = bar0 + 112, vote = bar0 + 120;
+  static_assert(Y::kStagesK <= 4 && Y::kStagesV <= 3 && kParts <= 3, "barriers");
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + Y::kOffBar + 256);
+  volatile int* const flag = reinterpret_cast<volatile int*>(smem + Y::kOffBar + 272 + str * 8);  // [2]
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + Y::kOffBar + 264);
+  long long* const tbl = reinterpret_cast<long long*>(smem + Y::kOffTbl);
+  if (!issuer && tid == 0) {
+    for (int i = 0; i < Y::kStagesK; ++i) mbar_init(full_k(i), 1);
+    for (int i = 0; i < Y::kStagesV; ++i) mbar_init(full_v(i), 1);
+    for (int h = 0; h < kParts; ++h) {
+      mbar_init(ready(h), Y::kW);
+      mbar_init(done(h), 1);
     }
-    mbar_init(a_ready, 4);
-    mbar_init(mma_done, 1);
-    bad_flag[0] = bad_flag[1] = 0;
-    if (grp == 0) *abort_flag = 0;
+    mbar_init(pv_ready, Y::kW);
+    mbar_init(pv_done, 1);
+    mbar_init(vote, Y::kW);
+    flag[0] = flag[1] = 0;
+    if (str == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == kGroups * 4 - 1) {
+  if (warp == 1) {
     tile_table(tbl, p.batch, lane, [&](int s) {
       const int ctx = p.seq_lens[s];
-      if (blockIdx.x == 0 && (ctx < 1 || ctx > p.max_seq_len))
-        atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+      if (blockIdx.x == 0 && (ctx < p.q_len || ctx > p.max_seq_len)) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
       return span_of(p, ctx).nt;
     });
     if (blockIdx.x == 0 && p.ws_tbl)
@@ -188,243 +241,312 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot + grp * kColGroup, 0);  // (known uniform)
-  const uint32_t t_lane = tmem + (uint32_t(gw * 32) << 16);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot + str * Y::kColStream, 0);  // (known uniform)
 
-  // ---- this group's piece of the line
+  // ---- this stream's piece of the line
   const long long total = tbl[p.batch] * p.hkv;
-  const int w = grp * gridDim.x + blockIdx.x;
+  const int w = str * gridDim.x + blockIdx.x;
   long long a = 0, b = 0;
-  if (grp >= kGroups) {
+  if (str >= Y::kStreams) {
     // the issuing warpgroup's idle warps
   } else if (total > 0 && p.whole_units) {
-    const long long units = (long long)p.batch * p.hkv;
-    const int W = int(units < p.workers ? units : p.workers);
-    auto at = [&](long long u) {
-      const int s = int(u / p.hkv);
-      return s >= p.batch ? total : tbl[s] * p.hkv + (u - (long long)s * p.hkv) * (tbl[s + 1] - tbl[s]);
+    const int units = p.batch * p.hkv, W = min(units, p.workers);
+    auto at = [&](int u) {
+      const int s = u / p.hkv;
+      return s >= p.batch ? total : tbl[s] * p.hkv + (u - s * p.hkv) * (tbl[s + 1] - tbl[s]);
     };
     if (w < W) {
       a = at(w * units / W);
       b = at((w + 1) * units / W);
     }
   } else if (total > 0) {
+    // (total fits 31 bits, W * W too: w total / W without a 64-bit division)
     const int W = pieces_of(total, p.min_tiles, p.workers);
+    const unsigned each = unsigned(total) / W, rest = unsigned(total) - each * W;
     if (w < W) {
-      a = w * total / W;
-      b = (w + 1) * total / W;
+      a = (long long)w * each + w * rest / W;
+      b = (long long)(w + 1) * each + (w + 1) * rest / W;
     }
   }
   const int n_all = int(b - a);
   auto wait_w = [&](uint32_t bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, MIMO_STATUS_TIMEOUT));
   };
-  auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); };
-  // A barrier at which a warp whose wait ran out takes the whole group with it.  The flags
-  // alternate: a warp ahead of the others writes the other one.
-  int tick = 0;
-  auto group_sync_ok = [&](bool good) -> bool {
-    if (!good && lane == 0) bad_flag[tick & 1] = 1;
-    group_sync();
-    const bool ok = bad_flag[tick & 1] == 0;
-    ++tick;
-    return ok;
-  };
 
   if (issuer) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Y::kRegsIssue));
     if (n_all > 0) {
-      // ---- copies of the piece's tiles in order, kStages ahead, and each tile's products
-      TileCursor ic = cursor_at(tbl, p.batch, p.hkv, a);
-      int pg_s = -1, pg_base = 0, pg = 0, it0 = 0;  // lane i: page id of page pg_base + i of sequence pg_s
-      // what lanes 0..3 copy: key codes, key scales, value scales (bulk copies), value codes (a TMA tile)
-      const int lane_bytes = lane == 0 ? kI4KCodes : (lane == 1 ? 2 * kI4KGroups : 2 * kI4VGroups);
-      const uint32_t lane_dst = lane == 0 ? kOffK : (lane == 1 ? kOffKs : kOffVs);
-      const int lane_block = kPage * (lane < 2 ? kI4KSlot : kI4VSlot);
-      const uint8_t* const lane_src =
-          lane == 0 ? p.k_cache : (lane == 1 ? p.k_cache + kPage * kI4KCodes : p.v_cache + kPage * kI4VCodes);
-      auto copy = [&](int n) {  // tile n of the piece
-        if (ic.t == ic.nt) next_unit(tbl, p.hkv, ic);
-        if (ic.s != pg_s) it0 = span_of(p, p.seq_lens[ic.s]).t0;
-        const int pi = it0 + ic.t;
-        if (ic.s != pg_s || pi < pg_base || pi >= pg_base + 32) {
-          pg_s = ic.s;
-          pg_base = pi;
+      // ---- copies of the piece's tiles in order, and each tile's products.  A slot of keys is free
+      // when the last part of its logits may run, one of values when its product may.
+      struct Copies {
+        TileCursor c;
+        int n, pg_s, pg_base, pg, t0;  // tiles copied; lane i: page id of page pg_base + i of sequence pg_s
+      };
+      Copies ck, cv;
+      ck.c = cv.c = cursor_at(tbl, p.batch, p.hkv, a);
+      ck.n = cv.n = ck.pg = cv.pg = ck.t0 = cv.t0 = ck.pg_base = cv.pg_base = 0;
+      ck.pg_s = cv.pg_s = -1;
+      auto next_block = [&](Copies& k) {  // of tile k.n of the piece
+        if (k.c.t == k.c.nt) next_unit(tbl, p.hkv, k.c);
+        if (k.c.s != k.pg_s) k.t0 = span_of(p, p.seq_lens[k.c.s]).t0;
+        const int pi = k.t0 + k.c.t;
+        if (k.c.s != k.pg_s || pi < k.pg_base || pi >= k.pg_base + 32) {
+          k.pg_s = k.c.s;
+          k.pg_base = pi;
           const int mine = pi + lane;
-          pg = 0;
-          if (mine < it0 + ic.nt) {
-            pg = mine < p.max_pages ? p.block_table[long(ic.s) * p.max_pages + mine] : -1;
-            if (pg < 0 || pg >= p.num_pages) {
+          k.pg = 0;
+          if (mine < k.t0 + k.c.nt) {
+            k.pg = mine < p.max_pages ? p.block_table[long(k.c.s) * p.max_pages + mine] : -1;
+            if (k.pg < 0 || k.pg >= p.num_pages) {
               atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-              pg = 0;
+              k.pg = 0;
             }
           }
         }
-        const int block = __shfl_sync(0xffffffffu, pg, pi - pg_base) * p.hkv + ic.g;
-        const uint32_t dst = ring0 + n % kStages * kStage, bar = full(n % kStages);
-        if (lane == 0) mbar_expect_tx(bar, kStage);
-        __syncwarp();
-        if (lane < 3) bulk_load(dst + lane_dst, lane_src + long(block) * lane_block, kTile * lane_bytes, bar);
-        else if (lane == 3) tma_load_3d(dst, &p.tm_v, bar, 0, 0, block);
-        __syncwarp();
-        ++ic.t;
+        ++k.c.t;
+        ++k.n;
+        return __shfl_sync(0xffffffffu, k.pg, pi - k.pg_base) * p.hkv + k.c.g;
       };
-      // a tile's products: the offset over all columns, then two steps per group
-      const uint64_t qd = sdesc_sw128(qt, 16, 1024), qo = sdesc_sw32(qt + kQOffset, 256);
-      const uint32_t qd_lo = uint32_t(qd), qd_hi = uint32_t(qd >> 32);
-      auto products = [&]() {
-        tc_fence_after();
-        tc_mma_ts(tmem + kColD, tmem + kColOne, qo, idesc_f32acc(128, kCols, 0, 0, 0), 0u);
-        product_steps<0>(tmem, qd_lo, qd_hi);
-        tc_commit(mma_done);
-      };
-      int copied = 0, done = 0;
-      bool ok = true;
-      for (; copied < n_all && copied < kStages; ++copied) copy(copied);
-      for (; done < n_all && ok; ++done) {
-        if (!(ok = wait_w(a_ready, done & 1))) break;
-        if (elect_one()) products();
-        __syncwarp();
-        // the stage of tile done - 2 is read: its next copy
-        if (done >= 2 && copied < n_all) {
-          if (!(ok = wait_w(empty(copied % kStages), (copied / kStages - 1) & 1))) break;
-          copy(copied++);
+      auto copy_k = [&]() {
+        if (ck.n >= n_all) return;
+        const int i = ck.n % Y::kStagesK;
+        const uint32_t dst = ring_k + i * kKBytes, bar = full_k(i);
+        const int block = next_block(ck);
+        if (elect_one()) {  // a block's codes and scales are one piece
+          mbar_expect_tx(bar, kKBytes);
+          bulk_load(dst, p.k_cache + long(block) * kPage * kI4KSlot, kKBytes, bar);
         }
+        __syncwarp();
+      };
+      auto copy_v = [&]() {
+        if (cv.n >= n_all) return;
+        const int i = cv.n % Y::kStagesV;
+        const uint32_t dst = ring_v + i * kVBytes, bar = full_v(i);
+        const int block = next_block(cv);
+        if (elect_one()) {
+          mbar_expect_tx(bar, kVBytes);
+          tma_load_3d(dst, &p.tm_v, bar, 0, 0, block);
+          bulk_load(dst + kOffVs, p.v_cache + long(block) * kPage * kI4VSlot + kOffVs, kTile * 2 * kI4VGroups, bar);
+        }
+        __syncwarp();
+      };
+      const uint64_t qd = sdesc_sw128(base, 16, 1024), qo = sdesc_sw32(base + Y::kQOffset, 256);
+      const uint64_t vd = sdesc_sw128(vt, Y::kVChunk, 1024);
+      const uint64_t pd = N == 16 ? sdesc_sw32(pt, 256) : sdesc_sw128(pt, Y::kVChunk, 1024);
+      constexpr int kPStep = N == 16 ? 16 * 32 : 16 * 128;  // bytes of a 16-key step of the weights
+      bool ok = true;
+      auto part = [&](auto pt_, int tile) {
+        constexpr int PT = decltype(pt_)::value;
+        if (!ok || !(ok = wait_w(ready(PT), tile & 1))) return;
+        if (elect_one()) {
+          tc_fence_after();
+          logits_part<N, PT>(tmem, qd, qo);
+          tc_commit(done(PT));
+        }
+        __syncwarp();
+        if (PT == kParts - 1) copy_k();
+      };
+      auto first_part = [&](int tile) { part(Int<0>(), tile); };
+      auto other_parts = [&](int tile) {
+        if constexpr (!Y::kSep) {
+          part(Int<1>(), tile);
+          if constexpr (kParts == 3) part(Int<2>(), tile);
+        }
+      };
+      for (int i = 0; i < Y::kStagesK; ++i) copy_k();
+      for (int i = 0; i < Y::kStagesV; ++i) copy_v();
+      TileCursor mc = cursor_at(tbl, p.batch, p.hkv, a);
+      int n = 0;
+      first_part(0);
+      for (; n < n_all && ok; ++n) {
+        if (mc.t == mc.nt) next_unit(tbl, p.hkv, mc);
+        const bool first = n == 0 || mc.t == 0;  // of the unit's tiles here: the sums start
+        ++mc.t;
+        const bool last = mc.t == mc.nt || n + 1 == n_all;  // (the next tile waits for its unit's query)
+        other_parts(n);
+        if (!last) first_part(n + 1);
+        if (!ok || !(ok = wait_w(pv_ready, n & 1))) break;
+        if (elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_ss(tmem + Y::kColO, vd + ((kk * 2048) >> 4), pd + ((kk * kPStep) >> 4), idesc_f32acc(128, N, 1, 1, 0),
+                      first && kk == 0 ? 0u : 1u);
+          tc_commit(pv_done);
+        }
+        __syncwarp();
+        copy_v();
+        if (last && n + 1 < n_all) first_part(n + 1);
       }
       if (!ok && elect_one()) {
         // a wait ran out: the copies and products under way end before the block does
         int dummy = 0;
-        for (int i = copied > kStages ? copied - kStages : 0; i < copied; ++i)
-          mbar_wait(full(i % kStages), (i / kStages) & 1, &dummy, nullptr, 0, 50000000ull);
-        tc_commit(mma_done);
-        for (int i = 0; i < 2; ++i) mbar_wait(mma_done, (done + i) & 1, &dummy, nullptr, 0, 50000000ull);
+        auto drain = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, &dummy, nullptr, 0, 50000000ull); };
+        for (int i = max(0, ck.n - Y::kStagesK); i < ck.n; ++i) drain(full_k(i % Y::kStagesK), (i / Y::kStagesK) & 1);
+        for (int i = max(0, cv.n - Y::kStagesV); i < cv.n; ++i) drain(full_v(i % Y::kStagesV), (i / Y::kStagesV) & 1);
+        tc_commit(pv_done);
+        for (int i = 1; i >= 0; --i) drain(pv_done, (n + i) & 1);
       }
     }
     tc_fence_before();
     __syncthreads();
     return;
   }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
-  TileCursor c;
-  if (n_all > 0) c = cursor_at(tbl, p.batch, p.hkv, a);
 
-  // the constant row of A: 2^-14 (times the offset operand's -8 sum / 2^8 / ... : int4.cuh)
-  if (n_all > 0) {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Y::kRegsWork));
+  const uint32_t t_lane = tmem + (uint32_t(gq * 32) << 16);
+  auto stream_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(str + 1), "n"(Y::kN) : "memory"); };
+  // A barrier that tells whether any thread of the stream brought `v`.
+  auto any_of = [&](bool v) -> bool {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(v)), "r"(str + 1), "n"(Y::kN)
+        : "memory");
+    return r != 0;
+  };
+  if (hw == 0 && n_all > 0) {
     uint32_t one[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) one[i] = 0x04000400u;
-    tmem_st8(t_lane + kColOne, one);
+    for (int i = 0; i < 8; ++i) one[i] = 0x04000400u;  // 2^-14
+    tmem_st8(t_lane + Y::kColOne, one);
     tmem_wait_st();
-    if (NB == 1) {  // heads 8..15 of the P rows: none
-      const uint32_t z[4] = {0, 0, 0, 0};
-      sts128(pt + lane * kPRow + 16, z);
-    }
   }
-
-  // Key of this thread, unpacked into its row of A.
-  auto unpack = [&](uint32_t stage) {
-    uint32_t W[24];
-    const uint32_t ka = stage + kOffK + (gw * 32 + lane) * kI4KCodes;
+  const int row = gq * 32 + lane;  // this thread's key of the tile
+  const uint32_t v_row = vt + row * 128 + ((row & 7) << 4);
+  constexpr int kQ = 4 / kT;  // words of a thread per group
+  uint32_t W[6 * kQ], zs[3];           // this thread's part of the next tile's key: word 4 j + kQ hw + q of group j at 6 q + j; its scales
+  int kst = 0, kph = 0, vst = 0, vph = 0;
+  auto fetch = [&]() -> bool {
+    if (!wait_w(full_k(kst), kph & 1)) return false;
+    const uint32_t at = ring_k + kst * kKBytes, ka = at + row * kI4KCodes + 24 * kQ * hw;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) lds128(ka + 16 * i, W + 4 * i);
+    for (int i = 0; i < 3; ++i) {
+      if constexpr (kQ == 2) lds128(ka + 16 * i, W + 4 * i);
+      else lds64(ka + 8 * i, W + 2 * i);
+    }
 #pragma unroll
-    for (int j = 0; j < kI4KGroups; ++j) {
-      uint32_t r[16];
+    for (int i = 0; i < 3; ++i) zs[i] = lds32(at + kOffKs + row * 2 * kI4KGroups + 4 * i);
+    if (++kst == Y::kStagesK) kst = 0, ++kph;
+    return true;
+  };
+  // Part h of it into the key's row of A.
+  auto unpack = [&](int h) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+    for (int j = kPer * h; j < kPer * h + kPer; ++j) {
+      uint32_t r[4 * kQ];
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
         const uint32_t x = W[6 * q + j], y = x >> 8;
         r[4 * q] = x & kI4Lo;
         r[4 * q + 1] = x & kI4Hi;
         r[4 * q + 2] = y & kI4Lo;
         r[4 * q + 3] = y & kI4Hi;
       }
-      tmem_st16(t_lane + kColA + 16 * j, r);
+      if constexpr (kQ == 2) tmem_st8(t_lane + Y::kColA + 16 * j + 8 * hw, r);
+      else tmem_st4(t_lane + Y::kColA + 16 * j + 4 * hw, r);
     }
     tmem_wait_st();
   };
-  // ... and hands it to the issuing warp, the sums of the tile before read
-  auto hand_over = [&]() {
+  auto hand_over = [&](uint32_t bar) {
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(a_ready);
+    if (lane == 0) mbar_arrive(bar);
   };
-
+  uint32_t k1024, k64;
+  asm volatile("mov.b32 %0, 0x64006400;\n\tmov.b32 %1, 0x54005400;" : "=r"(k1024), "=r"(k64));  // (opaque: see field)
+  const int G = p.group, g_log = G == 16 ? 4 : 3, rows = p.q_len * G;
   const float c_log2 = p.scale_log2 * kI4KeyUnit;
   const uint64_t c2 = pack_f32x2(c_log2, c_log2);
-  uint32_t flip;
-  asm volatile("mov.b32 %0, 0xFFFF0000;" : "=r"(flip));  // (opaque, or it is folded into a second instruction)
-  const uint32_t sign = (lane & 1) ? 0x80008000u : 0u;  // odd keys enter as -p * (15 - code)
-  uint32_t tb[kI4VGroups];  // (-8, -7) in the columns of group u, else 0
-#pragma unroll
-  for (int u = 0; u < kI4VGroups; ++u) tb[u] = (r0 & 3) == u ? 0xC700C800u : 0u;
-
-  int st = 0, ph = 0;
   bool ok = true;
+  TileCursor c;
+  if (n_all > 0) c = cursor_at(tbl, p.batch, p.hkv, a);
   for (int x = 0; x < n_all && ok;) {
     if (c.t == c.nt) next_unit(tbl, p.hkv, c);
-    const int s = c.s, g = c.g, t_first = c.t;
+    const int s = c.s, g = c.g, t_first = c.t, ctx = p.seq_lens[s];
     const int t_end = min(c.nt, c.t + (n_all - x));
-    const int ctx = p.seq_lens[s];
     const Span U = span_of(p, ctx);
-    // ---- the unit's query operand: 8 threads per head, thread r of them dims 4 r .. 4 r + 3, their
-    // rotary partners 32 + 4 r .., and 64 + 16 r .. 64 + 16 r + 15
+    const int first_pos = ctx - p.q_len;  // slot of the first draft
+    // ---- the unit's query operand: 8 threads a row, thread r dims 4 r .. 4 r + 3, their rotary
+    // partners, and 64 + 16 r .. 64 + 16 r + 15
+    constexpr int kRows = Y::kN / 8, kPasses = (N + kRows - 1) / kRows;
+    const int r = lane & 7;
+    uint2 ra[kPasses], rb[kPasses];
+    uint4 rc[kPasses][2];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int n = i * kRows + (tid >> 3);
+      ra[i] = rb[i] = make_uint2(0, 0);
+      rc[i][0] = rc[i][1] = make_uint4(0, 0, 0, 0);
+      if (n < rows) {
+        const uint16_t* q = p.q + ((long(s) * p.q_len + (n >> g_log)) * kHq + g * G + (n & (G - 1))) * kDqk;
+        ra[i] = __ldg(reinterpret_cast<const uint2*>(q + 4 * r));
+        rb[i] = __ldg(reinterpret_cast<const uint2*>(q + 32 + 4 * r));
+        rc[i][0] = __ldg(reinterpret_cast<const uint4*>(q + 64 + 16 * r));
+        rc[i][1] = __ldg(reinterpret_cast<const uint4*>(q + 64 + 16 * r) + 1);
+      }
+    }
+    stream_sync();  // (the unit before has read what is written here)
     {
-      const int h = (threadIdx.x & 127) >> 3, r = lane & 7;
-      float cs, sn;
-      rope_cos_sin(p.positions ? p.positions[s] : ctx - 1, p.rope.inv_freq[lane], &cs, &sn);
-      const uint16_t* row = p.q + (long(s) * kHq + g * G + h) * kDqk;
-      uint2 ra = make_uint2(0, 0), rb = ra;
-      uint4 rc[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (NB == 2 || h < 8) {
-        ra = __ldg(reinterpret_cast<const uint2*>(row + 4 * r));
-        rb = __ldg(reinterpret_cast<const uint2*>(row + 32 + 4 * r));
-        rc[0] = __ldg(reinterpret_cast<const uint4*>(row + 64 + 16 * r));
-        rc[1] = __ldg(reinterpret_cast<const uint4*>(row + 64 + 16 * r) + 1);
-      }
-      float v[24];
-      {
-        const uint32_t wa[2] = {ra.x, ra.y}, wb[2] = {rb.x, rb.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float xa = (i & 1) ? hi_bf16(wa[i >> 1]) : lo_bf16(wa[i >> 1]);
-          const float xb = (i & 1) ? hi_bf16(wb[i >> 1]) : lo_bf16(wb[i >> 1]);
-          const float ci = __shfl_sync(0xffffffffu, cs, 4 * r + i), si = __shfl_sync(0xffffffffu, sn, 4 * r + i);
-          v[i] = xa * ci - xb * si;
-          v[4 + i] = xb * ci + xa * si;
-        }
-        const uint32_t wc[8] = {rc[0].x, rc[0].y, rc[0].z, rc[0].w, rc[1].x, rc[1].y, rc[1].z, rc[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[8 + 2 * i] = lo_bf16(wc[i]);
-          v[9 + 2 * i] = hi_bf16(wc[i]);
-        }
-      }
-      // element k (the position of a dim) of row `row` of the operand part at `at`
-      auto elem = [&](int at, int row, int k) {
-        return qt + at + row * 128 + ((((k & 63) >> 3) ^ (row & 7)) << 4) + (k & 7) * 2;
-      };
-      // the offset rows: 4096 bytes of zeros, 32 a thread
+      const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
+      for (int i = tid; i < p.q_len * kHalf; i += Y::kN)
+        rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
+      if (tid < N) nref[tid] = tid < rows ? INFINITY : -INFINITY;  // (a padding column: weight 0)
       const uint32_t zero[4] = {0, 0, 0, 0};
+      for (int i = tid; i < kI4KGroups * N * 2; i += Y::kN) sts128(base + Y::kQOffset + 16 * i, zero);
+    }
+    stream_sync();
+    float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) sts128(qt + kQOffset + (threadIdx.x & 127) * 32 + 16 * i, zero);
-      float amax = 0.f, s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    for (int i = 0; i < kPasses; ++i) {
+      const int n = i * kRows + (tid >> 3);
+      if (n >= N) break;  // (warp-uniform)
+      // 8 dims: fields come out of a word as (0, 4), (1, 5), (2, 6), (3, 7), the odd ones times 16 (* 4, / 4)
+      auto put = [&](const float* v, int chunk, int unit, bool two) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int i = 0; i < 24; i += 2) {
-        // dims d and d + 1: an even and an odd field (* 4, / 4)
-        const int d = i < 4 ? 4 * r + i : (i < 8 ? 32 + 4 * r + i - 4 : 64 + 16 * r + i - 8);
-        const uint32_t hw = pack2_f16_sat(v[i] * 4.f, v[i + 1] * 0.25f, amax);
-        // k of dim d: fields come out of a word as (0, 4), (1, 5), (2, 6), (3, 7)
-        const int k0 = (d & ~7) + 2 * (d & 3) + ((d >> 2) & 1), k1 = k0 + 2;
-        const int at = i < 8 ? 0 : (r < 4 ? kQOff1 : kQOff2);
-        sts16(elem(at, h, k0), uint16_t(hw));
-        sts16(elem(at, h, k1), uint16_t(hw >> 16));
-        if (i < 8) {
-          const float2 t = f32x2_of_f16x2(hw);
-          const uint32_t lw = f16x2_of(v[i] * 4.f - t.x, v[i + 1] * 0.25f - t.y);
-          sts16(elem(0, 16 + h, k0), uint16_t(lw));
-          sts16(elem(0, 16 + h, k1), uint16_t(lw >> 16));
+        for (int e = 0; e < 4; ++e) {
+          const float f = (e & 1) ? 0.25f : 4.f;
+          hi[e] = pack2_f16_sat(v[e] * f, v[e + 4] * f, amax);
+          if (two) {
+            const float2 t = f32x2_of_f16x2(hi[e]);
+            lo[e] = f16x2_of(v[e] * f - t.x, v[e + 4] * f - t.y);
+          }
         }
-        (i < 4 ? s0 : (i < 8 ? s1 : s2)) += v[i] + v[i + 1];
+        const uint32_t at = base + n * 128 + ((unit ^ (n & 7)) << 4);
+        sts128(at + chunk * Y::kQChunk, hi);
+        if (two) sts128(at + 3 * Y::kQChunk, lo);
+      };
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+      {
+        // rotated: even threads end up with 8 dims of the first half, odd ones with 8 of the second
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t wa = e < 2 ? ra[i].x : ra[i].y, wb = e < 2 ? rb[i].x : rb[i].y;
+          const float xa = (e & 1) ? hi_bf16(wa) : lo_bf16(wa), xb = (e & 1) ? hi_bf16(wb) : lo_bf16(wb);
+          const float2 t = cs[min(n >> g_log, p.q_len - 1) * kHalf + 4 * r + e];
+          const float a0 = xa * t.x - xb * t.y, b0 = xb * t.x + xa * t.y;
+          s0 += a0;
+          s1 += b0;
+          const float other = __shfl_xor_sync(0xffffffffu, (r & 1) ? a0 : b0, 1);
+          v[e] = (r & 1) ? other : a0;
+          v[4 + e] = (r & 1) ? b0 : other;
+        }
+        put(v, 0, (r >> 1) + 4 * (r & 1), true);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w4[4] = {rc[i][h].x, rc[i][h].y, rc[i][h].z, rc[i][h].w};
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = lo_bf16(w4[e]);
+          v[2 * e + 1] = hi_bf16(w4[e]);
+          s2 += v[2 * e] + v[2 * e + 1];
+        }
+        put(v, 1 + (r >> 2), 2 * (r & 3) + h, false);
       }
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) {
@@ -432,312 +554,276 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
         s1 += __shfl_xor_sync(0xffffffffu, s1, d);
         if (d == 1) s2 += __shfl_xor_sync(0xffffffffu, s2, d);
       }
-      group_sync();  // (the zeros are written)
       auto offset = [&](int j, float sum) {
-        // -8 sum in the sums' unit 2^-22, over the constant 2^-14: elements 0 and 1 of the column's row
+        // -8 sum in the sums' unit 2^-22, over the constant 2^-14, as two terms
         const float o = sum * -0.03125f;
         const uint32_t hi = f16x2_of(o, 0.f), lo = f16x2_of(o - f32x2_of_f16x2(hi).x, 0.f);
-        const int row = col_of(j) + h;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(qt + kQOffset + row * 32 + (((row >> 2) & 1) << 4)), "r"(hi | (lo << 16))
+        const int col = j * N + n;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + Y::kQOffset + col * 32 + (((col >> 2) & 1) << 4)), "r"(hi | (lo << 16))
                      : "memory");
       };
       if (r == 0) offset(0, s0);
       if (r == 1) offset(1, s1);
       if ((r & 1) == 0) offset(2 + (r >> 1), s2);
-      if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
-      fence_proxy_async_smem();
     }
-    group_sync();  // every warp's part of the operand is written
-    bool good = wait_w(full(st), ph & 1);
+    if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
+    fence_proxy_async_smem();
+    stream_sync();
+    bool good = fetch();
+    uint32_t z[3];
     if (good) {
-      unpack(ring0 + st * kStage);
-      hand_over();
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) unpack(h);
+      hand_over(ready(0));
     }
-    uint64_t nref[H2];    // minus this warp's references, alike in all lanes
-    uint64_t l2[H2];      // this thread's sums, heads 2 i and 2 i + 1
-    float o[kI4VGroups][4][4], T[4] = {0.f, 0.f, 0.f, 0.f};  // T: column n holds group n % 4's offset
+    constexpr bool kHold = N <= 64;  // the references in registers
+    auto ref2 = [&](int i) { return *reinterpret_cast<const uint64_t*>(nref + hw * NC + 2 * i); };
+    uint64_t nr[kHold ? NC / 2 : 1];
+    if constexpr (kHold)
 #pragma unroll
-    for (int i = 0; i < H2; ++i) {
-      nref[i] = pack_f32x2(INFINITY, INFINITY);
-      l2[i] = 0;
-    }
+      for (int i = 0; i < NC / 2; ++i) nr[i] = ref2(i);
+    uint64_t l[NC / 2];  // this thread's sums of its columns
 #pragma unroll
-    for (int u = 0; u < kI4VGroups; ++u)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[u][e][0] = o[u][e][1] = o[u][e][2] = o[u][e][3] = 0.f;
+    for (int i = 0; i < NC / 2; ++i) l[i] = 0;
 
-    for (; c.t < t_end && good; ++c.t, ++x) {
-      const uint32_t stage = ring0 + st * kStage;
-      const int key0 = (U.t0 + c.t) * kTile + gw * 32;  // this warp's keys
-      const bool live = key0 <= U.hi && key0 + 31 >= U.lo;
-      const bool edge = key0 < U.lo || key0 + 31 > U.hi;
-      if (!(good = wait_w(mma_done, x & 1))) break;
-      tc_fence_after();
-      // ---- logits of this thread's key
-      uint64_t S[H2];
+    for (; c.t < t_end; ++c.t, ++x) {
+      const int key = (U.t0 + c.t) * kTile + row, key0 = key - lane;
+      // a column's draft d sees the keys first_pos + d - window + 1 .. first_pos + d of [lo, hi]
+      const bool edge = key0 < U.lo + (p.window > 0 ? p.q_len - 1 : 0) || key0 + 31 > min(U.hi, first_pos);
+      const bool more = c.t + 1 < t_end, start = c.t == t_first;
 #pragma unroll
-      for (int i = 0; i < H2; ++i) S[i] = 0;
-      if (live) {
-        uint32_t z[3];
+      for (int i = 0; i < 3; ++i) z[i] = zs[i];
+      uint64_t S[NC / 2];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) z[i] = lds32(stage + kOffKs + (gw * 32 + lane) * 2 * kI4KGroups + 4 * i);
-        // two blocks of columns at a time: both terms of group 0, of group 1, then groups 2..5
+      for (int i = 0; i < NC / 2; ++i) S[i] = 0;
 #pragma unroll
-        for (int b2 = 0; b2 < 4; ++b2) {
-          uint32_t d[2][16];
+      for (int h = 0; h < kParts; ++h) {
+        if (good) good = wait_w(done(h), x & 1);
+        if (!good) continue;
+        tc_fence_after();
+        constexpr int kC = NC == 16 ? 16 : 8;  // columns at a time
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if constexpr (NB == 2) tmem_ld16(t_lane + kColD + 32 * b2 + 16 * i, d[i]);
-            else tmem_ld8(t_lane + kColD + 32 * b2 + 16 * i, d[i]);
+        for (int c0 = 0; c0 < NC; c0 += kC) {
+          uint32_t d[kPer][kC];
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const uint32_t at = t_lane + Y::col(kPer * h + j) + hw * NC + c0;
+            if constexpr (kC == 16) tmem_ld16(at, d[j]);
+            else tmem_ld8(at, d[j]);
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if constexpr (NB == 2) tmem_wait_ld_r16(d[i]);
-            else tmem_wait_ld_r8(d[i]);
-            const int j = b2 < 2 ? b2 : 2 * b2 - 2 + i;
-            const float2 zz = f32x2_of_f16x2(z[j >> 1]);
-            const float sc = (j & 1) ? zz.y : zz.x;
+          for (int j = 0; j < kPer; ++j) {
+            if (j > 0) tied<kC>(d[j]);  // (one wait is for all)
+            else if constexpr (kC == 16) tmem_wait_ld_r16(d[j]);
+            else tmem_wait_ld_r8(d[j]);
+            const float2 zz = f32x2_of_f16x2(z[(kPer * h + j) >> 1]);
+            const float sc = ((kPer * h + j) & 1) ? zz.y : zz.x;
             const uint64_t s2 = pack_f32x2(sc, sc);
 #pragma unroll
-            for (int e = 0; e < H2; ++e)
-              S[e] = fma_f32x2(pack_f32x2(__uint_as_float(d[i][2 * e]), __uint_as_float(d[i][2 * e + 1])), s2, S[e]);
+            for (int i = 0; i < kC / 2; ++i)
+              S[c0 / 2 + i] = fma_f32x2(pack_f32x2(__uint_as_float(d[j][2 * i]), __uint_as_float(d[j][2 * i + 1])), s2, S[c0 / 2 + i]);
+          }
+        }
+        if (h + 1 < kParts) hand_over(ready(h + 1));  // (its columns are free)
+        if (more) {
+          if (h == 0) good = fetch();
+          if (good) unpack(h);
+        }
+        if (good && more && h == kParts - 1) hand_over(ready(0));
+      }
+      // ---- logits against the references, 8 columns at a time (of one draft)
+      auto logits = [&](int i, float* xs) {
+        uint64_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = kHold ? nr[kHold ? 4 * i + e : 0] : ref2(4 * i + e);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t v = fma_f32x2(S[4 * i + e], c2, r[e]);
+          xs[2 * e] = lo_f32(v);
+          xs[2 * e + 1] = hi_f32(v);
+        }
+      };
+      auto hidden = [&](int i) {
+        const int at = first_pos + ((hw * NC + 8 * i) >> g_log);
+        return key > min(at, U.hi) || (p.window > 0 && key <= at - p.window);
+      };
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NC / 8; ++i) {
+        float xs[8], t8 = -INFINITY;
+        logits(i, xs);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t8 = fmaxf(t8, xs[e]);
+        if (edge && hidden(i)) t8 = -INFINITY;
+        top = fmaxf(top, t8);
+      }
+      // (the warps tell each other which tile moves the references; the answer is read after the values)
+      const bool raise = __any_sync(0xffffffffu, top > kSlack) || !good;
+      if (lane == 0) {
+        if (raise) flag[x & 1] = x + 1;
+        mbar_arrive(vote);
+      }
+      // ---- values: (code - 8) * scale in fp16, this thread's groups.  1024 + n and 64 + n come out of a
+      // word with one LOP3; the scale is not folded into the weights, as a row of 64 dims has two.
+      // A slot nothing was written to may hold any scale: it counts as 0
+      // (where the logits run in parts, the last one's sums stand after the product of the tile before)
+      if (Y::kSep && good && x > 0) good = wait_w(pv_done, (x - 1) & 1);
+      if (good) good = wait_w(full_v(vst), vph & 1);
+      if (good) {
+        const uint32_t at = ring_v + vst * kVBytes;
+#pragma unroll
+        for (int u = 0; u < kQ; ++u) {
+          const int j = hw * kQ + u;  // group
+          const uint32_t sv = key <= U.hi ? lds16(at + kOffVs + row * 2 * kI4VGroups + 2 * j) : 0u, s2 = sv | (sv << 16);
+          uint32_t vw[4];
+          lds128(at + row * kI4VCodes + ((j ^ ((row >> 1) & 3)) << 4), vw);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t y = vw[i] >> 8;
+            uint32_t o[4];
+            o[0] = hmul2(hadd2(field(vw[i], kI4Lo, k1024), 0xE408E408u), s2);  // - 1032
+            o[1] = hmul2(hadd2(field(vw[i], kI4Hi, k64), 0xD480D480u), s2);    // - 72
+            o[2] = hmul2(hadd2(field(y, kI4Lo, k1024), 0xE408E408u), s2);
+            o[3] = hmul2(hadd2(field(y, kI4Hi, k64), 0xD480D480u), s2);
+            sts128((v_row ^ ((4 * (j & 1) + i) << 4)) + (j >> 1) * Y::kVChunk, o);
           }
         }
       }
-      // ---- the next tile's keys: its products run behind this tile's softmax
-      int nst = st + 1, nph = ph;
-      if (nst == kStages) nst = 0, ++nph;
-      if (c.t + 1 < t_end) {
-        if (!(good = wait_w(full(nst), nph & 1))) break;
-        unpack(ring0 + nst * kStage);
-        hand_over();
+      if (++vst == Y::kStagesV) vst = 0, ++vph;
+      // (every warp arrives, its own waits being bounded)
+      for (int i = 0; i < 1000000 && !mbar_try_wait_hint(vote, x & 1, 20000); ++i) {
       }
-      if (live) {
-        // ---- weights
-        const bool valid = key0 + lane >= U.lo && key0 + lane <= U.hi;
-        float xs[G];
-        float top = -INFINITY;
-        auto logits = [&]() {
-          top = -INFINITY;
+      if (flag[x & 1] == x + 1) {
+        // the references that were passed move to their new maxima, and the sums with them
 #pragma unroll
-          for (int i = 0; i < H2; ++i) {
-            const uint64_t v = fma_f32x2(S[i], c2, nref[i]);
-            xs[2 * i] = lo_f32(v);
-            xs[2 * i + 1] = hi_f32(v);
-          }
-          if (edge && !valid) {
-#pragma unroll
-            for (int i = 0; i < G; ++i) xs[i] = -INFINITY;
-          }
-#pragma unroll
-          for (int i = 0; i < G; ++i) top = fmaxf(top, xs[i]);
-        };
-        logits();
-        if (__any_sync(0xffffffffu, top > kSlack)) {
-          // move the references that were passed to their new maxima, and the sums with them
-          float al[G];
-#pragma unroll
-          for (int i = 0; i < G; ++i) {
-            float z = ((i & 1) ? hi_f32(S[i >> 1]) : lo_f32(S[i >> 1])) * c_log2;
-            if (edge && !valid) z = -INFINITY;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, d));
-            const float ref = -((i & 1) ? hi_f32(nref[i >> 1]) : lo_f32(nref[i >> 1]));
-            const bool up = z > ref + kSlack;
-            al[i] = up ? ex2(ref - z) : 1.f;  // (from -inf: 0, of sums that are 0)
-            const float now = up ? -z : -ref;
-            nref[i >> 1] = (i & 1) ? pack_f32x2(lo_f32(nref[i >> 1]), now) : pack_f32x2(now, hi_f32(nref[i >> 1]));
-          }
-          float* const ax = xch + gw * 32;
-          if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < G; ++i) ax[i] = al[i];
-          __syncwarp();
-          const float a0 = ax[r0], a1 = NB == 2 ? ax[8 + r0] : 0.f;
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < H2; ++i) l2[i] = mul_f32x2(l2[i], pack_f32x2(al[2 * i], al[2 * i + 1]));
-#pragma unroll
-          for (int u = 0; u < kI4VGroups; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[u][e][0] *= a0;
-              o[u][e][1] *= a0;
-              o[u][e][2] *= a1;
-              o[u][e][3] *= a1;
-            }
-          T[0] *= a0;
-          T[1] *= a0;
-          T[2] *= a1;
-          T[3] *= a1;
-          logits();
+        for (int i = 0; i < NC; ++i) {
+          float m = ((i & 1) ? hi_f32(S[i >> 1]) : lo_f32(S[i >> 1])) * c_log2;
+          if (edge && hidden(i >> 3)) m = -INFINITY;
+          m = warp_max(m);
+          if (lane == 0) wmax[gq * N + hw * NC + i] = m;
         }
-        uint32_t pk[H2];
-#pragma unroll
-        for (int i = 0; i < H2; ++i) {
-          const float p0 = ex2(xs[2 * i]), p1 = ex2(xs[2 * i + 1]);
-          l2[i] = add_f32x2(l2[i], pack_f32x2(p0, p1));
-          pk[i] = f16x2_of(p0, p1) ^ sign;
+        if (any_of(!good)) {
+          ok = false;
+          break;
         }
-        sts128(pt + lane * kPRow, pk);
-        if constexpr (NB == 2) sts128(pt + lane * kPRow + 16, pk + 4);
-        __syncwarp();
-        // ---- O += P V over this warp's 32 keys
+        if (tid < N) {
+          const float m = fmaxf(fmaxf(wmax[tid], wmax[N + tid]), fmaxf(wmax[2 * N + tid], wmax[3 * N + tid]));
+          const float ref = -nref[tid];
+          const bool up = m > ref + kSlack;
+          fac[tid] = up ? ex2(ref - m) : 1.f;  // (from -inf: 0, of sums that are 0)
+          if (up) nref[tid] = -m;
+        }
+        stream_sync();
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          uint32_t P[4];
-          ldsm_x4_t(pt + (16 * kk + (lane >> 4) * 8 + (lane & 7)) * kPRow + ((lane >> 3) & 1) * 16, P);
-          // value scales of keys 2 q4, 2 q4 + 1 of either 8: [group] fp16 pairs.  A slot nothing was
-          // written to may hold any scale: it counts as 0
-          uint32_t vs[2][kI4VGroups];
+        for (int i = 0; i < NC / 2; ++i) l[i] = mul_f32x2(l[i], *reinterpret_cast<const uint64_t*>(fac + hw * NC + 2 * i));
+        if constexpr (kHold)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t h[4];
-            const int k8 = 16 * kk + 8 * e + 2 * q4;
-            lds128(stage + kOffVs + (gw * 32 + k8) * 2 * kI4VGroups, h);
-            vs[e][0] = __byte_perm(h[0], h[2], 0x5410);
-            vs[e][1] = __byte_perm(h[0], h[2], 0x7632);
-            vs[e][2] = __byte_perm(h[1], h[3], 0x5410);
-            vs[e][3] = __byte_perm(h[1], h[3], 0x7632);
-            if (edge) {
+          for (int i = 0; i < NC / 2; ++i) nr[i] = ref2(i);
+        if (!start) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < NC; c0 += 8) {
+            uint32_t d[8];
+            tmem_ld8(t_lane + Y::kColO + hw * NC + c0, d);
+            tmem_wait_ld_r8(d);
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (key0 + k8 + i > U.hi)
-#pragma unroll
-                  for (int u = 0; u < kI4VGroups; ++u) vs[e][u] &= i ? 0x0000FFFFu : 0xFFFF0000u;
-            }
+            for (int i = 0; i < 8; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) * fac[hw * NC + c0 + i]);
+            tmem_st8(t_lane + Y::kColO + hw * NC + c0, d);
           }
-          const int row = gw * 32 + 16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-          for (int up = 0; up < 2; ++up) {
-            uint32_t m[4];
-            ldsm_x4_t(stage + row * kI4VCodes + (((2 * up + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), m);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int u = 2 * up + h;
-              uint32_t pa[4];
-              pa[0] = hmul2(P[0], vs[0][u]);
-              pa[1] = hmul2(P[1], vs[0][u]);
-              pa[2] = hmul2(P[2], vs[1][u]);
-              pa[3] = hmul2(P[3], vs[1][u]);
-              const uint32_t x0 = m[2 * h], x1 = m[2 * h + 1], y0 = x0 >> 8, y1 = x1 >> 8;
-              // (the odd key's codes complemented)
-              mma_f16_acc(o[u][0], pa, field(x0, flip, kI4Lo), field(x1, flip, kI4Lo));
-              mma_f16_acc(o[u][1], pa, field(x0, flip, kI4Hi), field(x1, flip, kI4Hi));
-              mma_f16_acc(o[u][2], pa, field(y0, flip, kI4Lo), field(y1, flip, kI4Lo));
-              mma_f16_acc(o[u][3], pa, field(y0, flip, kI4Hi), field(y1, flip, kI4Hi));
-              // p (n - 8) = p n - 8 p for the even key, -p (15 - n) + 7 p for the odd one
-              mma_f16_acc(T, pa, tb[u], tb[u]);
-            }
-          }
+          tmem_wait_st();
         }
       }
-      __syncwarp();  // (P is read before the next tile writes it)
-      if (lane == 0) mbar_arrive(empty(st));
-      st = nst;
-      ph = nph;
+      // ---- weights
+#pragma unroll
+      for (int i = 0; i < NC / 8; ++i) {
+        float xs[8];
+        logits(i, xs);
+        if (edge && hidden(i)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xs[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xs[e] = ex2(xs[e]);
+        uint32_t pk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pk[e] = f16x2_of(xs[2 * e], xs[2 * e + 1]);
+          l[4 * i + e] = add_f32x2(l[4 * i + e], pack_f32x2(xs[2 * e], xs[2 * e + 1]));
+        }
+        const int c8 = hw * (NC / 8) + i;  // of 8 columns
+        if constexpr (N == 16) sts128(pt + row * 32 + ((c8 ^ ((row >> 2) & 1)) << 4), pk);
+        else sts128(pt + (c8 >> 3) * Y::kVChunk + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), pk);
+      }
+      if (good) {
+        fence_proxy_async_smem();
+        hand_over(pv_ready);
+      }
     }
-    // a warp whose wait ran out takes the group with it here
-    if (!(ok = group_sync_ok(good))) break;
+    if (!ok) break;
 
-    // ---- the segment's rows: the four warps' sums against the largest of their references
-    {
-      float* const ax = xch + gw * 32;
+    // ---- the segment's rows: this thread holds one dim of its columns' sums
+    if (good) good = wait_w(pv_done, (x - 1) & 1);
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        float v = (i & 1) ? hi_f32(l2[i >> 1]) : lo_f32(l2[i >> 1]);
+    for (int c0 = 0; c0 < NC / 8; ++c0) {
+      // 8 sums over the warp: a step halves what a lane holds, down to one column per 4 lanes
+      float v[8];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (lane == 0) {
-          ax[i] = -((i & 1) ? hi_f32(nref[i >> 1]) : lo_f32(nref[i >> 1]));
-          ax[16 + i] = v;
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = lo_f32(l[4 * c0 + e]);
+        v[2 * e + 1] = hi_f32(l[4 * c0 + e]);
+      }
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) {
+        const bool up = lane & (4 * d);
+#pragma unroll
+        for (int e = 0; e < d; ++e) {
+          const float got = __shfl_xor_sync(0xffffffffu, up ? v[e] : v[e + d], 4 * d);
+          v[e] = (up ? v[e + d] : v[e]) + got;
         }
       }
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+      if ((lane & 3) == 0) wmax[gq * N + hw * NC + 8 * c0 + (lane >> 2)] = v[0];
     }
-    group_sync();
-    float M[2], L[2], fac[2];  // heads r0 and 8 + r0
-#pragma unroll
-    for (int hf = 0; hf < NB; ++hf) {
-      const int h = r0 + 8 * hf;
-      M[hf] = fmaxf(fmaxf(xch[h], xch[32 + h]), fmaxf(xch[64 + h], xch[96 + h]));
-      L[hf] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float rf = xch[32 * i + h], f = rf == -INFINITY ? 0.f : ex2(rf - M[hf]);
-        L[hf] += f * xch[32 * i + 16 + h];
-        if (i == gw) fac[hf] = f;
-      }
+    if (any_of(!good)) {
+      ok = false;
+      break;
     }
+    tc_fence_after();
     const bool direct = t_first == 0 && c.t == c.nt;
     const long piece = 2L * w + (x > c.t - t_first ? 1 : 0);  // this worker's first or last segment
-    // 2 KB blocks of the group's query operand and P rows (both free now): [warp][group of a round]
-    auto block = [&](int i) {
-      return reinterpret_cast<float4*>(i < 6 ? smem + grp * kQBytes + 2048 * i
-                                             : smem + kOffP + grp * 4 * kPBytes + 2048 * (i - 6));
-    };
-    static_assert(4 * kPBytes >= 2 * 2048 && kQBytes >= 6 * 2048, "merge room");
-#pragma unroll
-    for (int round = 0; round < 2; ++round) {
-#pragma unroll
-      for (int ur = 0; ur < 2; ++ur) {
-        const int u = 2 * round + ur;
-        float4* const dst = block(gw * 2 + ur);
-#pragma unroll
-        for (int hf = 0; hf < NB; ++hf) {
-          // T's columns 0..3 are in lanes 0 and 1 of the quad
-          const float t = __shfl_sync(0xffffffffu, T[2 * hf + (u & 1)], (lane & ~3) + (u >> 1));
-          float f[8];  // dims 32 u + 8 q4 + i of head r0 + 8 hf
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = fmaf(o[u][i & 3][2 * hf + (i >> 2)], (i & 1) ? 0x1p20f : 0x1p24f, t) * fac[hf];
-          dst[(2 * hf) * 32 + lane] = make_float4(f[0], f[1], f[2], f[3]);
-          dst[(2 * hf + 1) * 32 + lane] = make_float4(f[4], f[5], f[6], f[7]);
+    if (tid < rows) {
+      const int n = tid, h = g * G + (n & (G - 1));
+      const float M = -nref[n], L = wmax[n] + wmax[N + n] + wmax[2 * N + n] + wmax[3 * N + n];
+      if (direct) {
+        float M2 = M, L2 = L, f = 1.f;
+        if (p.sink) {
+          const float sl = p.sink[h] * kLog2e;
+          M2 = fmaxf(M, sl);
+          f = ex2(M - M2);
+          L2 = L * f + ex2(sl - M2);
         }
+        fac[n] = p.v_scale * f / L2;
+        if (p.lse) p.lse[(long(s) * p.q_len + (n >> g_log)) * kHq + h] = (M2 + log2f(L2)) * kLn2;
+      } else {
+        *reinterpret_cast<float2*>(p.ws_ml + (piece * (p.n_blocks * 16) + n) * 2) = make_float2(M, L);
       }
-      group_sync();
-      if ((gw >> 1) == round) {
-        const int u = gw;
-#pragma unroll
-        for (int hf = 0; hf < NB; ++hf) {
-          float4 v[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 t = block(2 * i + (gw & 1))[(2 * hf + e) * 32 + lane];
-              v[e].x += t.x;
-              v[e].y += t.y;
-              v[e].z += t.z;
-              v[e].w += t.w;
-            }
-          }
-          const int rr = r0 + 8 * hf, h = g * G + rr, dim = 32 * u + 8 * q4;
-          if (direct) {
-            float M2 = M[hf], L2 = L[hf], f = 1.f;
-            if (p.sink) {
-              const float sl = p.sink[h] * kLog2e;
-              M2 = fmaxf(M[hf], sl);
-              f = ex2(M[hf] - M2);
-              L2 = L[hf] * f + ex2(sl - M2);
-            }
-            const float sc = p.v_scale * f / L2;
-            if (p.lse && u == 0 && q4 == 0) p.lse[long(s) * kHq + h] = (M2 + log2f(L2)) * kLn2;
-            *reinterpret_cast<uint4*>(p.out + (long(s) * kHq + h) * kDv + dim) =
-                make_uint4(pack2_bf16(v[0].x * sc, v[0].y * sc), pack2_bf16(v[0].z * sc, v[0].w * sc),
-                           pack2_bf16(v[1].x * sc, v[1].y * sc), pack2_bf16(v[1].z * sc, v[1].w * sc));
-          } else {
-            if (u == 0 && q4 == 0) *reinterpret_cast<float2*>(p.ws_ml + (piece * 16 + rr) * 2) = make_float2(M[hf], L[hf]);
-            float4* dst = reinterpret_cast<float4*>(p.ws_o + (piece * 16 + rr) * kDv + dim);
-            dst[0] = v[0];
-            dst[1] = v[1];
-          }
-        }
-      }
-      group_sync();
     }
-    if (NB == 1) {  // the merge used the P rows: heads 8..15 are none again
-      const uint32_t z[4] = {0, 0, 0, 0};
-      sts128(pt + lane * kPRow + 16, z);
+    stream_sync();
+    const int dim = (row & ~7) + ((row & 7) >> 1) + 4 * (row & 1);
+#pragma unroll 1
+    for (int n0 = hw * NC; n0 < min(rows, hw * NC + NC); n0 += 8) {  // 8 heads of a draft
+      uint32_t d[8];
+      tmem_ld8(t_lane + Y::kColO + n0, d);
+      tmem_wait_ld_r8(d);
+      if (direct) {
+        uint16_t* const at = p.out + ((long(s) * p.q_len + (n0 >> g_log)) * kHq + g * G + (n0 & (G - 1))) * kDv + dim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at[i * kDv] = uint16_t(pack2_bf16(__uint_as_float(d[i]) * fac[n0 + i], 0.f));
+      } else {
+        float* const at = p.ws_o + (piece * (p.n_blocks * 16) + n0) * kDv + dim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at[i * kDv] = __uint_as_float(d[i]);
+      }
     }
   }
   tc_fence_before();
@@ -748,12 +834,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_tc_kernel(const __grid_co
   }
 }
 
-cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s) {
-  auto kernel = p.hkv == 8 ? decode4_tc_kernel<1> : decode4_tc_kernel<2>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+namespace {
+template <int N>
+cudaError_t launch_n(const Decode4Params& p, int sms, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(decode4_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<N>::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<p.workers < sms ? p.workers : sms, kThreads, kSmem, s>>>(p);
+  decode4_tc_kernel<N><<<p.workers < sms ? p.workers : sms, Lay<N>::kThreads, Lay<N>::kSmem, s>>>(p);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s) {
+  const int rows = p.q_len * p.group;
+  if (rows <= 16) return launch_n<16>(p, sms, s);
+  if (rows <= 32) return launch_n<32>(p, sms, s);
+  if (rows <= 64) return launch_n<64>(p, sms, s);
+  if (rows <= 96) return launch_n<96>(p, sms, s);
+  return launch_n<128>(p, sms, s);
 }
 
 }  // namespace mimo

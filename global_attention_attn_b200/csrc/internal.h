@@ -74,14 +74,13 @@ struct DecodeParams {
 };
 
 // Decode over a 4-bit cache (decode_int4.cu).
-constexpr int kI4Tile = 32;        // keys per tile of the draft kernel
-constexpr int kI4TcTile = 128;     // and of the one-token kernel
-constexpr int kI4TcGroups = 2;     // workers per CTA there
+constexpr int kI4Tile = 32;        // keys per tile of a ring
+constexpr int kI4TcTile = 128;     // and of pages
 constexpr int kMaxTableBatch = 1024;  // sequences per launch (a prefix table in shared memory)
 struct Decode4Params {
   CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, tile, 1}
   int batch, hkv, group, q_len, n_blocks;
-  int one;                     // the one-token kernel
+  int tc;                      // decode_int4_tc.cu (pages), else decode_int4.cu (rings)
   int nc, groups, stages;      // draft kernel: warps per worker (one per row block), workers per CTA, stages per worker
   int workers, min_tiles;      // workers at most; tiles a worker takes at least
   int whole_units;             // pieces hold whole (sequence, KV head) units: no combine
@@ -106,7 +105,7 @@ struct Decode4Params {
   unsigned* status;
 };
 struct Decode4Plan {
-  int one;  // the one-token kernel
+  int tc;
   int tile, n_blocks, nc, groups, stages, workers, min_tiles, whole_units;
 };
 

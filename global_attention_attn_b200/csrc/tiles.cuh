@@ -52,9 +52,9 @@ __device__ __forceinline__ TileCursor cursor_at(const long long* tbl, int batch,
   TileCursor c;
   c.s = lo;
   c.nt = int(tbl[lo + 1] - tbl[lo]);
-  const long long rem = x - tbl[lo] * hkv;
-  c.g = int(rem / c.nt);
-  c.t = int(rem - (long long)c.g * c.nt);
+  const unsigned rem = unsigned(x - tbl[lo] * hkv);  // (at most hkv * nt)
+  c.g = int(rem / unsigned(c.nt));
+  c.t = int(rem - c.g * unsigned(c.nt));
   return c;
 }
 // The next unit that has tiles (the caller knows there is one).
