@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
   }
   const int n_all = int(b - a);
   auto wait_w = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // (a branch of the whole warp)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, MIMO_STATUS_TIMEOUT));
   };
 
