@@ -273,14 +273,12 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   p.groups = plan.groups;
   p.stages = plan.stages;
   p.workers = plan.workers;
-  p.min_tiles = plan.min_tiles;
   p.whole_units = plan.whole_units;
   p.window = a->layer.window;
   p.max_seq_len = a->max_seq_len;
   p.scale_log2 = a->layer.softmax_scale * 1.4426950408889634f;
   p.v_scale = a->layer.v_scale;
   p.sink = a->layer.sink;
-  p.cache_kind = a->cache_kind;
   p.ring_slots = ring_slots;
   p.max_pages = a->max_pages;
   p.num_pages = a->num_pages;

@@ -1,6 +1,7 @@
-// Decode over a 4-bit ring and draft verification (2..8 query tokens per sequence) over a 4-bit
-// ring or paged cache: the attention of decode.cu on the cache format of int4.cuh; the paged
-// one-token decode's host side (decode_int4_tc.cu) and the combine kernel of both.
+// Decode and draft verification (1..8 query tokens per sequence) over a 4-bit ring: the attention
+// of decode.cu on the cache format of int4.cuh.  Also the host side of decode_int4_tc.cu, which
+// takes the paged caches: its tile is 128 keys, and a ring of 128 to 512 slots is one to four of
+// those, a new query operand and an emptied pipeline before each ring.
 //
 // 180 bytes per (key, KV head) stand against 16 x 320 multiply-adds a draft (57 FLOP per byte),
 // and every element has to be unpacked first: unlike the wide caches this one is bound by
@@ -20,14 +21,11 @@
 //   - the rotated query dims enter as two fp16 terms: no 16-bit type holds them to the digits of
 //     an fp32 log-sum-exp.
 //
-// Workers are groups of nc warps (one per 16-row block of query rows, sharing the tiles).  The
-// tiles (32 keys) of all sequences and KV heads form one line, cut into as many equal pieces
-// as there are workers, so any mix of lengths loads every SM alike; a piece's first and last
-// (sequence, head) may be partial and go through the combine kernel, the others write their
-// rows directly.  Ring caches and short contexts are cut between (sequence, head) units only
-// and need no second kernel.  Each group's leader warp issues the copies of later tiles itself
-// (one bulk copy for the codes and for the scales, one TMA tile with the 64-byte swizzle for
-// the values); there are no producer warps, so all 8 warps multiply.
+// Workers are groups of nc warps (one per 16-row block of query rows, sharing the tiles of 32
+// keys), each of which takes whole (sequence, KV head) units and writes their rows.  Each group's
+// leader warp issues the copies of later tiles itself (one bulk copy for the codes and for the
+// scales, one TMA tile with the 64-byte swizzle for the values); there are no producer warps, so
+// all 8 warps multiply.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -41,7 +39,6 @@ namespace mimo {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kCombineWarps = 4;
 constexpr int kTile = kI4Tile;
 // stage: value codes (64-byte swizzle), key codes, key scales, value scales
 constexpr int kOffK = kTile * kI4VCodes, kOffKs = kOffK + kTile * kI4KCodes;
@@ -90,26 +87,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Keys a sequence's unit covers: [lo, end), and its first tile and tile count.
-struct Span {
-  int lo, end, t0, nt;
-};
-__device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
-  Span u;
-  u.end = p.cache_kind == MIMO_CACHE_RING ? ctx : min(ctx, p.max_seq_len);
-  u.lo = p.window > 0 ? max(0, ctx - p.q_len + 1 - p.window) : 0;
-  if (ctx < p.q_len || u.lo >= u.end) {
-    u.t0 = u.nt = 0;
-  } else if (p.cache_kind == MIMO_CACHE_RING) {
-    u.t0 = 0;
-    u.nt = (p.ring_slots + kTile - 1) / kTile;
-  } else {
-    u.t0 = u.lo / kTile;
-    u.nt = (u.end - 1) / kTile - u.t0 + 1;
-  }
-  return u;
-}
-
 }  // namespace
 
 __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_constant__ Decode4Params p) {
@@ -134,44 +111,31 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     fence_mbar_init();
   }
   if (warp == kWarps - 1) {
+    const int ring_tiles = (p.ring_slots + kTile - 1) / kTile;
     tile_table(tbl, p.batch, lane, [&](int s) {
-      const int ctx = p.seq_lens[s];
-      if (blockIdx.x == 0 && (ctx < p.q_len || (ctx > p.max_seq_len && p.cache_kind != MIMO_CACHE_RING)))
-        atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-      return span_of(p, ctx).nt;
+      const bool bad = p.seq_lens[s] < p.q_len;
+      if (blockIdx.x == 0 && bad) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+      return bad ? 0 : ring_tiles;
     });
-    if (blockIdx.x == 0 && p.ws_tbl)
-      for (int s = lane; s <= p.batch; s += 32) p.ws_tbl[s] = tbl[s];
   }
   __syncthreads();
   if (grp >= p.groups) return;
   const long long total = tbl[p.batch] * p.hkv;
   if (total == 0) return;
   const int w = grp * gridDim.x + blockIdx.x;
-  long long a, b;
-  if (p.whole_units) {
-    // pieces of whole (sequence, head) units
-    const long long units = (long long)p.batch * p.hkv;
-    const int W = int(units < p.workers ? units : p.workers);
-    if (w >= W) return;
-    auto at = [&](long long u) {
-      const int s = int(u / p.hkv);
-      return s >= p.batch ? total : tbl[s] * p.hkv + (u - (long long)s * p.hkv) * (tbl[s + 1] - tbl[s]);
-    };
-    a = at(w * units / W);
-    b = at((w + 1) * units / W);
-  } else {
-    const int W = pieces_of(total, p.min_tiles, p.workers);
-    if (w >= W) return;
-    a = w * total / W;
-    b = (w + 1) * total / W;
-  }
+  const int units = p.batch * p.hkv, W = min(units, p.workers);
+  if (w >= W) return;
+  auto at = [&](int u) {
+    const int s = u / p.hkv;
+    return s >= p.batch ? total : tbl[s] * p.hkv + (u - s * p.hkv) * (tbl[s + 1] - tbl[s]);
+  };
+  const long long a = at(w * units / W), b = at((w + 1) * units / W);
   if (a >= b) return;
 
   const bool leader = blk == 0;
-  const bool ring = p.cache_kind == MIMO_CACHE_RING;
-  const int slots = ring ? p.ring_slots : kPage;  // of a block
+  const int slots = p.ring_slots;  // of a block
   auto wait_w = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // (a branch of the whole warp)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, MIMO_STATUS_TIMEOUT));
   };
 
@@ -180,7 +144,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
   TileCursor ic = start;
   int left = int(b - a);
   int ist = 0, iph = 0;         // stage and pass of the next copy
-  int pg_s = -1, pg_base = 0, pg = 0, it0 = 0;  // lane i: page id of page pg_base + i of sequence pg_s
   // what lanes 0..3 copy: key codes, key scales, value scales (bulk copies), value codes (a TMA tile)
   const int lane_bytes = lane == 0 ? kI4KCodes : (lane == 1 ? 2 * kI4KGroups : 2 * kI4VGroups);
   const uint32_t lane_dst = lane == 0 ? kOffK : (lane == 1 ? kOffKs : kOffVs);
@@ -191,29 +154,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     if (left == 0) return true;
     --left;
     if (ic.t == ic.nt) next_unit(tbl, p.hkv, ic);
-    int block, slot;
-    if (ring) {
-      block = int(p.block0) + ic.s * p.hkv + ic.g;
-      slot = ic.t * kTile;
-    } else {
-      if (ic.s != pg_s) it0 = span_of(p, p.seq_lens[ic.s]).t0;
-      const int key = (it0 + ic.t) * kTile, pi = key / kPage;
-      if (ic.s != pg_s || pi < pg_base || pi >= pg_base + 32) {
-        pg_s = ic.s;
-        pg_base = pi;
-        const int last = (it0 + ic.nt - 1) * kTile / kPage, mine = pi + lane;
-        pg = 0;
-        if (mine <= last) {
-          pg = mine < p.max_pages ? p.block_table[long(ic.s) * p.max_pages + mine] : -1;
-          if (pg < 0 || pg >= p.num_pages) {
-            atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-            pg = 0;
-          }
-        }
-      }
-      block = __shfl_sync(0xffffffffu, pg, pi - pg_base) * p.hkv + ic.g;
-      slot = key % kPage;
-    }
+    const int block = int(p.block0) + ic.s * p.hkv + ic.g, slot = ic.t * kTile;
     if (nc > 1 && iph > 0 && !wait_w(empty(ist), (iph - 1) & 1)) return false;
     const int n = min(kTile, slots - slot);
     const uint32_t dst = ring0 + ist * kStage, bar = full(ist);
@@ -242,17 +183,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
   // ---- every warp's side
   const int q4 = lane & 3, r0 = lane >> 2;
   const uint32_t rest0 = sbase + kOffRest + warp * 2048 + lane * 16;
-  const int G = p.group, rows = p.n_blocks * 16;
+  const int G = p.group;
   int st = 0, ph = 0;
   bool behind = false;  // nc > 1: a stage was released but its next copy is not issued yet
   TileCursor c = start;
   const int n_all = int(b - a);
   for (int x = 0; x < n_all && ok;) {
     if (c.t == c.nt) next_unit(tbl, p.hkv, c);
-    const int s = c.s, g = c.g, t_first = c.t;
-    const int t_end = min(c.nt, c.t + (n_all - x));
+    const int s = c.s, g = c.g;
     const int ctx = p.seq_lens[s];
-    const Span U = span_of(p, ctx);
     // rows r0 and r0 + 8 of the block: row 16 blk + r is draft (16 blk + r) / G
     int lo_r[2], hi_r[2], draft[2];
 #pragma unroll
@@ -262,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
       // (a padding row sees what the row before it sees: it calls for no mask of its own)
       const bool valid = draft[hf] < p.q_len;
       lo_r[hf] = valid ? (p.window > 0 ? max(0, at - p.window + 1) : 0) : lo_r[0];
-      hi_r[hf] = valid ? min(U.end - 1, at) : hi_r[0];
+      hi_r[hf] = valid ? at : hi_r[0];
     }
     // ---- query fragments (the second terms in shared memory), and those of the key offset's product
     uint32_t qa[2 * kI4KGroups][4];
@@ -344,8 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     }
     const float c_log2 = p.scale_log2 * kI4KeyUnit;
     const int R = p.ring_slots;
-    const int ring_off = ring ? ((R - ctx) % R + R) % R : 0;  // slot j holds position ctx - R + (j + ring_off) % R
-    const int lo_all = max(lo_r[0], lo_r[1]), hi_all = min(hi_r[0], hi_r[1]);
+    const int ring_off = ((R - ctx) % R + R) % R;  // slot j holds position ctx - R + (j + ring_off) % R
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
     float o[kI4VGroups][4][4], T[4] = {0.f, 0.f, 0.f, 0.f};  // T: column n holds group n % 4's offset
     uint32_t tb[kI4VGroups];  // (-8, -7) in the columns of group u, else 0
@@ -356,7 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
       tb[u] = (r0 & 3) == u ? 0xC700C800u : 0u;
     }
 
-    for (; c.t < t_end; ++c.t, ++x) {
+    for (; c.t < c.nt; ++c.t, ++x) {
       if (!(ok = wait_w(full(st), ph & 1))) break;
       {
         const uint32_t vb = ring0 + st * kStage, kb = vb + kOffK, ksb = vb + kOffKs, vsb = vb + kOffVs;
@@ -412,27 +350,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
           vs[nb][2] = __byte_perm(h[1], h[3], 0x5410);
           vs[nb][3] = __byte_perm(h[1], h[3], 0x7632);
         }
-        // ---- masks, only in tiles that some row does not see whole.  A slot nothing was written
-        // to may hold any scale: it counts as 0
-        const int key0 = (U.t0 + c.t) * kTile;
-        if (ring || key0 < lo_all || key0 + kTile - 1 > hi_all) {
+        // ---- masks.  A slot nothing was written to may hold any scale: it counts as 0
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb)
+        for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int col = 8 * nb + 2 * q4 + e;
-              int kp = key0 + col;
-              if (ring) {
-                const int j = kp + ring_off;
-                kp = kp < R ? ctx - R + (j >= R ? j - R : j) : -1;
-              }
-              if (!(kp >= 0 && kp < U.end))
+          for (int e = 0; e < 2; ++e) {
+            const int at = c.t * kTile + 8 * nb + 2 * q4 + e, j = at + ring_off;
+            const int kp = at < R ? ctx - R + (j >= R ? j - R : j) : -1;
+            if (kp < 0)
 #pragma unroll
-                for (int u = 0; u < kI4VGroups; ++u) vs[nb][u] &= e ? 0x0000FFFFu : 0xFFFF0000u;
-              if (!(kp >= lo_r[0] && kp <= hi_r[0])) S[nb][e] = -INFINITY;
-              if (!(kp >= lo_r[1] && kp <= hi_r[1])) S[nb][2 + e] = -INFINITY;
-            }
-        }
+              for (int u = 0; u < kI4VGroups; ++u) vs[nb][u] &= e ? 0x0000FFFFu : 0xFFFF0000u;
+            if (!(kp >= lo_r[0] && kp <= hi_r[0])) S[nb][e] = -INFINITY;
+            if (!(kp >= lo_r[1] && kp <= hi_r[1])) S[nb][2 + e] = -INFINITY;
+          }
         // ---- running maximum and sum
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -530,129 +460,47 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
       l_r[hf] += __shfl_xor_sync(0xffffffffu, l_r[hf], 1);
       l_r[hf] += __shfl_xor_sync(0xffffffffu, l_r[hf], 2);
     }
-    const bool direct = t_first == 0 && c.t == c.nt;
-    const long piece = 2L * w + (x > c.t - t_first ? 1 : 0);  // this worker's first or last segment
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       if (draft[hf] >= p.q_len) continue;
       const int rr = blk * 16 + r0 + 8 * hf, h = g * G + rr % G;
       const long qrow = long(s) * p.q_len + draft[hf];
       const float M = m_r[hf] - kPBias, L = l_r[hf];
-      float M2 = M, L2 = L, sc = 1.f;
-      if (direct) {
-        float f = 1.f;
-        if (p.sink) {
-          const float sl = p.sink[h] * kLog2e;
-          M2 = fmaxf(M, sl);
-          f = ex2(M - M2);
-          L2 = L * f + ex2(sl - M2);
-        }
-        sc = p.v_scale * f / L2;
-        if (p.lse && q4 == 0) p.lse[qrow * kHq + h] = (M2 + log2f(L2)) * kLn2;
-      } else if (q4 == 0) {
-        *reinterpret_cast<float2*>(p.ws_ml + (piece * rows + rr) * 2) = make_float2(M, L);
+      float M2 = M, L2 = L, f = 1.f;
+      if (p.sink) {
+        const float sl = p.sink[h] * kLog2e;
+        M2 = fmaxf(M, sl);
+        f = ex2(M - M2);
+        L2 = L * f + ex2(sl - M2);
       }
+      const float sc = p.v_scale * f / L2;
+      if (p.lse && q4 == 0) p.lse[qrow * kHq + h] = (M2 + log2f(L2)) * kLn2;
 #pragma unroll
       for (int u = 0; u < kI4VGroups; ++u) {
         float f[8];  // dims 32 u + 8 q4 + i
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           f[i] = fmaf(o[u][i & 3][2 * hf + (i >> 2)], (i & 1) ? 0x1p20f : 0x1p24f, t_off[hf][u]) * sc;
-        if (direct) {
-          *reinterpret_cast<uint4*>(p.out + (qrow * kHq + h) * kDv + 32 * u + 8 * q4) =
-              make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.ws_o + (piece * rows + rr) * kDv + 32 * u + 8 * q4);
-          dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-          dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
+        *reinterpret_cast<uint4*>(p.out + (qrow * kHq + h) * kDv + 32 * u + 8 * q4) =
+            make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
       }
     }
   }
   if (!ok) drain();
 }
 
-// One block per (query row, head): merges the pieces that share the row's unit.  A long context
-// of a small batch has hundreds, each a dependent load away: the warps take every fourth, and
-// the first warp adds up the warps' sums (a fixed order, whatever the timing).
-__global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
-  __shared__ float4 part[kCombineWarps][32];
-  __shared__ float part_m[kCombineWarps], part_l[kCombineWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qrow = blockIdx.x / kHq, h = blockIdx.x % kHq, s = qrow / p.q_len, g = h / p.group;
-  const long long total = p.ws_tbl[p.batch] * p.hkv;
-  const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
-  if (nt == 0) return;
-  const long long u0 = p.ws_tbl[s] * p.hkv + g * nt;
-  const int W = pieces_of(total, p.min_tiles, p.workers);
-  const int w0 = int(((u0 + 1) * W - 1) / total), w1 = int(((u0 + nt) * W - 1) / total);
-  if (w0 == w1) return;  // one piece holds the unit: its rows are written
-  const int rows = p.n_blocks * 16, rr = (qrow - s * p.q_len) * p.group + h % p.group;
-  // the first piece's unit is that piece's last segment, unless it begins with it
-  const long first = 2L * w0 + (u0 > w0 * total / W ? 1 : 0);
-  auto piece = [&](int i) { return (i == 0 ? first : 2L * (w0 + i)) * rows + rr; };
-  const int n = w1 - w0 + 1;
-  float M = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kCombineWarps * 32) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if (lane == 0) part_m[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kCombineWarps; ++i) M = fmaxf(M, part_m[i]);
-  float sl = -INFINITY;
-  if (p.sink) {
-    sl = p.sink[h] * kLog2e;
-    M = fmaxf(M, sl);
-  }
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = warp; i < n; i += kCombineWarps) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * piece(i));
-    const float f = ex2(ml.x - M);
-    const float4 v = *reinterpret_cast<const float4*>(p.ws_o + piece(i) * kDv + lane * 4);
-    L += f * ml.y;
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
-  }
-  part[warp][lane] = acc;
-  if (lane == 0) part_l[warp] = L;
-  __syncthreads();
-  if (warp > 0) return;
-#pragma unroll
-  for (int i = 1; i < kCombineWarps; ++i) {
-    const float4 v = part[i][lane];
-    L += part_l[i];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-  }
-  if (p.sink) L += ex2(sl - M);
-  const float sc = p.v_scale / L;
-  *reinterpret_cast<uint2*>(p.out + (long(qrow) * kHq + h) * kDv + lane * 4) =
-      make_uint2(pack2_bf16(acc.x * sc, acc.y * sc), pack2_bf16(acc.z * sc, acc.w * sc));
-  if (p.lse && lane == 0) p.lse[long(qrow) * kHq + h] = (M + log2f(L)) * kLn2;
-}
-
 Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms) {
   Decode4Plan d;
-  const bool tc = !ring;
+  d.tc = !ring;
+  d.tile = ring ? kI4Tile : kI4TcTile;
   d.n_blocks = (q_len * (kHq / hkv) + 15) / 16;
-  d.tile = tc ? kI4TcTile : kI4Tile;
   d.nc = d.n_blocks;
-  d.groups = tc ? (d.n_blocks == 1 ? 2 : 1) : kWarps / d.nc;
+  d.groups = ring ? kWarps / d.nc : (d.n_blocks == 1 ? 2 : 1);
   d.stages = kAllStages / d.groups;
   const int tiles = (unit_keys + d.tile - 1) / d.tile + 1;  // a window may begin inside a tile
   // A unit of up to 256 keys stays whole: a second kernel would cost more than it saves.
-  d.tc = tc;
   d.whole_units = ring || unit_keys <= 256;
-  d.min_tiles = tc ? 1 : 4;
-  const long long units = (long long)batch * hkv;
-  const long long most = d.whole_units ? units : (units * tiles + d.min_tiles - 1) / d.min_tiles;
+  const long long units = (long long)batch * hkv, most = d.whole_units ? units : units * tiles;
   d.workers = int(most < (long long)sms * d.groups ? most : (long long)sms * d.groups);
   return d;
 }
@@ -670,9 +518,7 @@ cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void
   }
   if (e != cudaSuccess) return e;
   if (ev_end && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_end), s)) != cudaSuccess) return e;
-  if (p.whole_units) return cudaSuccess;
-  decode4_combine_kernel<<<unsigned(p.batch * p.q_len * kHq), kCombineWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.whole_units ? cudaSuccess : launch_decode4_combine(p, s);
 }
 
 }  // namespace mimo

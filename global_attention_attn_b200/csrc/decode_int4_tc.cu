@@ -38,6 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Weights are 2^(z - ref): ref is a column's maximum when it was set, and moves only when a logit
 // passes it by more than this many powers of two.
 constexpr float kSlack = 6.f;
+constexpr int kCombineWarps = 4;
 
 // What depends on the number of columns.
 template <int N>
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
   }
   tc_fence_before();
   __syncthreads();
+  pdl_launch_dependents();  // (the combine: it waits for this grid's end)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot + str * Y::kColStream, 0);  // (known uniform)
 
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     }
   } else if (total > 0) {
     // (total fits 31 bits, W * W too: w total / W without a 64-bit division)
-    const int W = pieces_of(total, p.min_tiles, p.workers);
+    const int W = pieces_of(total, 1, p.workers);
     const unsigned each = unsigned(total) / W, rest = unsigned(total) - each * W;
     if (w < W) {
       a = (long long)w * each + w * rest / W;
@@ -852,6 +854,87 @@ cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s) {
   if (rows <= 64) return launch_n<64>(p, sms, s);
   if (rows <= 96) return launch_n<96>(p, sms, s);
   return launch_n<128>(p, sms, s);
+}
+
+// One block per (query row, head): merges the pieces that share the row's unit.  A long context
+// of a small batch has hundreds, each a dependent load away: the warps take every fourth, and
+// the first warp adds up the warps' sums (a fixed order, whatever the timing).
+__global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
+  __shared__ float4 part[kCombineWarps][32];
+  __shared__ float part_m[kCombineWarps], part_l[kCombineWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qrow = blockIdx.x / kHq, h = blockIdx.x % kHq, s = qrow / p.q_len, g = h / p.group;
+  pdl_wait_prerequisites();  // (launched behind the decode's start: its pieces stand from here on)
+  const long long total = p.ws_tbl[p.batch] * p.hkv;
+  const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
+  if (nt == 0) return;
+  const long long u0 = p.ws_tbl[s] * p.hkv + g * nt;
+  const int W = pieces_of(total, 1, p.workers);
+  const int w0 = int(((u0 + 1) * W - 1) / total), w1 = int(((u0 + nt) * W - 1) / total);
+  if (w0 == w1) return;  // one piece holds the unit: its rows are written
+  const int rows = p.n_blocks * 16, rr = (qrow - s * p.q_len) * p.group + h % p.group;
+  // the first piece's unit is that piece's last segment, unless it begins with it
+  const long first = 2L * w0 + (u0 > w0 * total / W ? 1 : 0);
+  auto piece = [&](int i) { return (i == 0 ? first : 2L * (w0 + i)) * rows + rr; };
+  const int n = w1 - w0 + 1;
+  float M = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += kCombineWarps * 32) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if (lane == 0) part_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) M = fmaxf(M, part_m[i]);
+  float sl = -INFINITY;
+  if (p.sink) {
+    sl = p.sink[h] * kLog2e;
+    M = fmaxf(M, sl);
+  }
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = warp; i < n; i += kCombineWarps) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * piece(i));
+    const float f = ex2(ml.x - M);
+    const float4 v = *reinterpret_cast<const float4*>(p.ws_o + piece(i) * kDv + lane * 4);
+    L += f * ml.y;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+  part[warp][lane] = acc;
+  if (lane == 0) part_l[warp] = L;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int i = 1; i < kCombineWarps; ++i) {
+    const float4 v = part[i][lane];
+    L += part_l[i];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  if (p.sink) L += ex2(sl - M);
+  const float sc = p.v_scale / L;
+  *reinterpret_cast<uint2*>(p.out + (long(qrow) * kHq + h) * kDv + lane * 4) =
+      make_uint2(pack2_bf16(acc.x * sc, acc.y * sc), pack2_bf16(acc.z * sc, acc.w * sc));
+  if (p.lse && lane == 0) p.lse[long(qrow) * kHq + h] = (M + log2f(L)) * kLn2;
+}
+
+
+cudaError_t launch_decode4_combine(const Decode4Params& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.batch * p.q_len * kHq));
+  cfg.blockDim = dim3(kCombineWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode4_combine_kernel, p);
 }
 
 }  // namespace mimo

@@ -81,8 +81,8 @@ struct Decode4Params {
   CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, tile, 1}
   int batch, hkv, group, q_len, n_blocks;
   int tc;                      // decode_int4_tc.cu (pages), else decode_int4.cu (rings)
-  int nc, groups, stages;      // draft kernel: warps per worker (one per row block), workers per CTA, stages per worker
-  int workers, min_tiles;      // workers at most; tiles a worker takes at least
+  int nc, groups, stages;      // rings: warps per worker (one per row block), workers per CTA, stages per worker
+  int workers;                 // at most
   int whole_units;             // pieces hold whole (sequence, KV head) units: no combine
   int window, max_seq_len;
   float scale_log2, v_scale;
@@ -90,7 +90,7 @@ struct Decode4Params {
   const uint16_t* q;
   const int32_t* seq_lens;
   const int32_t* positions;
-  int cache_kind, ring_slots;
+  int ring_slots;
   const uint8_t* k_cache;
   const uint8_t* v_cache;
   const int32_t* block_table;
@@ -106,7 +106,7 @@ struct Decode4Params {
 };
 struct Decode4Plan {
   int tc;
-  int tile, n_blocks, nc, groups, stages, workers, min_tiles, whole_units;
+  int tile, n_blocks, nc, groups, stages, workers, whole_units;
 };
 
 // Attention weights per cached slot (weights.cu).
@@ -244,6 +244,7 @@ void decode_rows(int q_len, int group, int* n_blocks, int* nc, int* n_rp);
 // unit_keys: keys a (sequence, KV head) covers at most
 Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring, int sms);
 cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s);
+cudaError_t launch_decode4_combine(const Decode4Params& p, cudaStream_t s);
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s);
 cudaError_t launch_weights_int4(WeightsParams p, int sms, cudaStream_t s);

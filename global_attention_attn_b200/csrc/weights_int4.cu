@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
   const long long a = blockIdx.x * total / gridDim.x, b = (blockIdx.x + 1) * total / gridDim.x;
   const int n_all = int(b - a);
   auto wait_w = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // (a branch of the whole warp)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, MIMO_STATUS_TIMEOUT));
   };
 
