@@ -18,9 +18,7 @@
 // the reference by 2^6 makes all of them move it; else nothing is rescaled.
 // Eight warps (two threads a key) work on a tile, a ninth issues copies and products.  One token of
 // a KV head is 16 columns: its tensor memory allows two such streams per SM, more columns one.
-#include "common.cuh"
-#include "int4.cuh"
-#include "ptx.cuh"
+#include "int4_tc.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
 
@@ -75,33 +73,6 @@ struct Lay {
   static_assert(kOffRingV % 512 == 0 && kSmem <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* r) {
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t a;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr) : "memory");
-  return a;
-}
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t* r) {
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-  uint16_t a;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(a) : "r"(addr) : "memory");
-  return a;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* r) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-}
-__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -111,12 +82,6 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
-}
-// Registers whose load a wait before has covered.
-template <int C>
-__device__ __forceinline__ void tied(uint32_t* d) {
-#pragma unroll
-  for (int i = 0; i < C; ++i) asm volatile("" : "+r"(d[i]));
 }
 __device__ __forceinline__ float warp_max(float v) {
   float m;
@@ -241,7 +206,6 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
   }
   tc_fence_before();
   __syncthreads();
-  pdl_launch_dependents();  // (the combine: it waits for this grid's end)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot + str * Y::kColStream, 0);  // (known uniform)
 
@@ -471,104 +435,16 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     const int t_end = min(c.nt, c.t + (n_all - x));
     const Span U = span_of(p, ctx);
     const int first_pos = ctx - p.q_len;  // slot of the first draft
-    // ---- the unit's query operand: 8 threads a row, thread r dims 4 r .. 4 r + 3, their rotary
-    // partners, and 64 + 16 r .. 64 + 16 r + 15
-    constexpr int kRows = Y::kN / 8, kPasses = (N + kRows - 1) / kRows;
-    const int r = lane & 7;
-    uint2 ra[kPasses], rb[kPasses];
-    uint4 rc[kPasses][2];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int n = i * kRows + (tid >> 3);
-      ra[i] = rb[i] = make_uint2(0, 0);
-      rc[i][0] = rc[i][1] = make_uint4(0, 0, 0, 0);
-      if (n < rows) {
-        const uint16_t* q = p.q + ((long(s) * p.q_len + (n >> g_log)) * kHq + g * G + (n & (G - 1))) * kDqk;
-        ra[i] = __ldg(reinterpret_cast<const uint2*>(q + 4 * r));
-        rb[i] = __ldg(reinterpret_cast<const uint2*>(q + 32 + 4 * r));
-        rc[i][0] = __ldg(reinterpret_cast<const uint4*>(q + 64 + 16 * r));
-        rc[i][1] = __ldg(reinterpret_cast<const uint4*>(q + 64 + 16 * r) + 1);
-      }
-    }
-    stream_sync();  // (the unit before has read what is written here)
-    {
-      const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
-      for (int i = tid; i < p.q_len * kHalf; i += Y::kN)
-        rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
-      if (tid < N) nref[tid] = tid < rows ? INFINITY : -INFINITY;  // (a padding column: weight 0)
-      const uint32_t zero[4] = {0, 0, 0, 0};
-      for (int i = tid; i < kI4KGroups * N * 2; i += Y::kN) sts128(base + Y::kQOffset + 16 * i, zero);
-    }
-    stream_sync();
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int n = i * kRows + (tid >> 3);
-      if (n >= N) break;  // (warp-uniform)
-      // 8 dims: fields come out of a word as (0, 4), (1, 5), (2, 6), (3, 7), the odd ones times 16 (* 4, / 4)
-      auto put = [&](const float* v, int chunk, int unit, bool two) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = (e & 1) ? 0.25f : 4.f;
-          hi[e] = pack2_f16_sat(v[e] * f, v[e + 4] * f, amax);
-          if (two) {
-            const float2 t = f32x2_of_f16x2(hi[e]);
-            lo[e] = f16x2_of(v[e] * f - t.x, v[e + 4] * f - t.y);
-          }
-        }
-        const uint32_t at = base + n * 128 + ((unit ^ (n & 7)) << 4);
-        sts128(at + chunk * Y::kQChunk, hi);
-        if (two) sts128(at + 3 * Y::kQChunk, lo);
-      };
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-      {
-        // rotated: even threads end up with 8 dims of the first half, odd ones with 8 of the second
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t wa = e < 2 ? ra[i].x : ra[i].y, wb = e < 2 ? rb[i].x : rb[i].y;
-          const float xa = (e & 1) ? hi_bf16(wa) : lo_bf16(wa), xb = (e & 1) ? hi_bf16(wb) : lo_bf16(wb);
-          const float2 t = cs[min(n >> g_log, p.q_len - 1) * kHalf + 4 * r + e];
-          const float a0 = xa * t.x - xb * t.y, b0 = xb * t.x + xa * t.y;
-          s0 += a0;
-          s1 += b0;
-          const float other = __shfl_xor_sync(0xffffffffu, (r & 1) ? a0 : b0, 1);
-          v[e] = (r & 1) ? other : a0;
-          v[4 + e] = (r & 1) ? b0 : other;
-        }
-        put(v, 0, (r >> 1) + 4 * (r & 1), true);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w4[4] = {rc[i][h].x, rc[i][h].y, rc[i][h].z, rc[i][h].w};
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = lo_bf16(w4[e]);
-          v[2 * e + 1] = hi_bf16(w4[e]);
-          s2 += v[2 * e] + v[2 * e + 1];
-        }
-        put(v, 1 + (r >> 2), 2 * (r & 3) + h, false);
-      }
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) {
-        s0 += __shfl_xor_sync(0xffffffffu, s0, d);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, d);
-        if (d == 1) s2 += __shfl_xor_sync(0xffffffffu, s2, d);
-      }
-      auto offset = [&](int j, float sum) {
-        // -8 sum in the sums' unit 2^-22, over the constant 2^-14, as two terms
-        const float o = sum * -0.03125f;
-        const uint32_t hi = f16x2_of(o, 0.f), lo = f16x2_of(o - f32x2_of_f16x2(hi).x, 0.f);
-        const int col = j * N + n;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + Y::kQOffset + col * 32 + (((col >> 2) & 1) << 4)), "r"(hi | (lo << 16))
-                     : "memory");
-      };
-      if (r == 0) offset(0, s0);
-      if (r == 1) offset(1, s1);
-      if ((r & 1) == 0) offset(2 + (r >> 1), s2);
-    }
+    // ---- the unit's query operand
+    const float amax = int4_query_operand<N, Y::kN, Y::kQChunk>(
+        p.q + (long(s) * p.q_len * kHq + g * G) * kDqk, rows, g_log, base, tid, cs, [&]() {
+          stream_sync();  // (the unit before has read what is written here)
+          const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
+          for (int i = tid; i < p.q_len * kHalf; i += Y::kN)
+            rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
+          if (tid < N) nref[tid] = tid < rows ? INFINITY : -INFINITY;  // (a padding column: weight 0)
+          stream_sync();
+        });
     if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
     fence_proxy_async_smem();
     stream_sync();
@@ -864,7 +740,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
   __shared__ float part_m[kCombineWarps], part_l[kCombineWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qrow = blockIdx.x / kHq, h = blockIdx.x % kHq, s = qrow / p.q_len, g = h / p.group;
-  pdl_wait_prerequisites();  // (launched behind the decode's start: its pieces stand from here on)
+  pdl_wait_prerequisites();  // (the pieces stand from here on)
   const long long total = p.ws_tbl[p.batch] * p.hkv;
   const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
   if (nt == 0) return;
@@ -924,6 +800,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
 }
 
 
+// Launched with programmatic serialization: its launch overlaps the decode's last blocks (131001 keys of one
+// sequence 42.5 -> 41.4 us; waiting on the SMs from the decode's start on it cost 45.3).
 cudaError_t launch_decode4_combine(const Decode4Params& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.batch * p.q_len * kHq));

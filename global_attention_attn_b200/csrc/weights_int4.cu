@@ -16,9 +16,7 @@
 // six 141: what bounds the kernel is instructions and the parts' handshakes, not the products;
 // with neither products nor reads of the sums it takes 88).  A ninth warp issues copies and
 // products.
-#include "common.cuh"
-#include "int4.cuh"
-#include "ptx.cuh"
+#include "int4_tc.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
 
@@ -46,42 +44,6 @@ constexpr int kSmem = kOffTbl + (kMaxTableBatch + 1) * 8 + 1024;
 static_assert(kSmem <= 232448 && kOffStage % 128 == 0 && kOffBar % 8 == 0, "shared memory budget");
 constexpr uint32_t kColA = 0, kColOne = 96, kColD = 128;
 constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* r) {
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// C columns (a multiple of 8) of this thread's row
-template <int C>
-__device__ __forceinline__ void cols_load(uint32_t at, uint32_t* d) {
-  if constexpr (C >= 16) {
-    tmem_ld16(at, d);
-    cols_load<C - 16>(at + 16, d + 16);
-  } else if constexpr (C >= 8) {
-    tmem_ld8(at, d);
-    cols_load<C - 8>(at + 8, d + 8);
-  }
-}
-template <int C>
-__device__ __forceinline__ void cols_wait(uint32_t* d) {
-  if constexpr (C >= 16) {
-    tmem_wait_ld_r16(d);
-    cols_wait<C - 16>(d + 16);
-  } else if constexpr (C >= 8) {
-    tmem_wait_ld_r8(d);
-    cols_wait<C - 8>(d + 8);
-  }
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t a;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr) : "memory");
-  return a;
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint16_t v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
-}
 
 // Steps KK .. of part PT of a tile's products, N columns a group (two terms for groups 0, 1).
 template <int N, int PT, int KK>
@@ -221,7 +183,7 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
         for (int i = copied > kStages ? copied - kStages : 0; i < copied; ++i)
           mbar_wait(full(i % kStages), (i / kStages) & 1, &dummy, nullptr, 0, 50000000ull);
         tc_commit(done(kParts - 1));
-        for (int i = 0; i < 2; ++i) mbar_wait(done(kParts - 1), (n + i) & 1, &dummy, nullptr, 0, 50000000ull);
+        for (int i = 1; i >= 0; --i) mbar_wait(done(kParts - 1), (n + i) & 1, &dummy, nullptr, 0, 50000000ull);
       }
     }
     tc_fence_before();
@@ -288,88 +250,22 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
     const int s = c.s, g = c.g, ctx = p.seq_lens[s], end = min(ctx, p.max_seq_len);
     const int t_end = min(c.nt, c.t + (n_all - x));
     // ---- the unit's query operand
-    const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_total + p.q_first;
-    for (int i = threadIdx.x; i < p.q_len * kHalf; i += kWork)
-      rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
-    if (threadIdx.x < N) {
-      // a row that attended nothing (or whose log-sum-exp is no number) adds nothing, nor does a padding column
-      float l = INFINITY;
-      if (threadIdx.x < rows) {
-        l = p.lse[(long(s) * p.q_total + p.q_first + threadIdx.x / G) * kHq + g * G + threadIdx.x % G];
-        l = fabsf(l) < INFINITY ? l * kLog2e : INFINITY;
-      }
-      lse2[threadIdx.x] = -l;  // (added to the logits)
-    }
-    // zeros for the offset rows' other elements
-    for (int i = threadIdx.x; i < 6 * N * 2; i += kWork)
-      asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sbase + kQOffset + 16 * i), "r"(0) : "memory");
-    all_sync();
-    float amax = 0.f;
-    // 8 threads a row: thread r dims 4 r .. 4 r + 3, their rotary partners, and 64 + 16 r .. 64 + 16 r + 15
-    for (int row = threadIdx.x >> 3; row < N; row += kWork / 8) {
-      const int r = lane & 7, dr = row / G;
-      float v[24];
-      if (row < rows) {
-        const uint16_t* q = p.q + ((long(s) * p.q_total + p.q_first + dr) * kHq + g * G + row % G) * kDqk;
-        const uint2 ra = __ldg(reinterpret_cast<const uint2*>(q + 4 * r)), rb = __ldg(reinterpret_cast<const uint2*>(q + 32 + 4 * r));
-        const uint4 c0 = __ldg(reinterpret_cast<const uint4*>(q + 64 + 16 * r)), c1 = __ldg(reinterpret_cast<const uint4*>(q + 64 + 16 * r) + 1);
-        const uint32_t wa[2] = {ra.x, ra.y}, wb[2] = {rb.x, rb.y};
-        const uint32_t wc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float xa = (i & 1) ? hi_bf16(wa[i >> 1]) : lo_bf16(wa[i >> 1]);
-          const float xb = (i & 1) ? hi_bf16(wb[i >> 1]) : lo_bf16(wb[i >> 1]);
-          const float2 t = cs[dr * kHalf + 4 * r + i];
-          v[i] = xa * t.x - xb * t.y;
-          v[4 + i] = xb * t.x + xa * t.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[8 + 2 * i] = lo_bf16(wc[i]);
-          v[9 + 2 * i] = hi_bf16(wc[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 24; ++i) v[i] = 0.f;
-      }
-      auto elem = [&](int chunk, int k) {
-        return sbase + chunk * kQChunk + row * 128 + ((((k & 63) >> 3) ^ (row & 7)) << 4) + (k & 7) * 2;
-      };
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 24; i += 2) {
-        // dims d and d + 1: an even and an odd field (* 4, / 4)
-        const int d = i < 4 ? 4 * r + i : (i < 8 ? 32 + 4 * r + i - 4 : 64 + 16 * r + i - 8);
-        const uint32_t h = pack2_f16_sat(v[i] * 4.f, v[i + 1] * 0.25f, amax);
-        const int k0 = (d & ~7) + 2 * (d & 3) + ((d >> 2) & 1), k1 = k0 + 2;
-        sts16(elem(d >> 6, k0), uint16_t(h));
-        sts16(elem(d >> 6, k1), uint16_t(h >> 16));
-        if (i < 8) {
-          const float2 t = f32x2_of_f16x2(h);
-          const uint32_t l = pack2_f16(v[i] * 4.f - t.x, v[i + 1] * 0.25f - t.y);
-          sts16(elem(3, k0), uint16_t(l));
-          sts16(elem(3, k1), uint16_t(l >> 16));
-        }
-        (i < 4 ? s0 : (i < 8 ? s1 : s2)) += v[i] + v[i + 1];
-      }
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) {
-        s0 += __shfl_xor_sync(0xffffffffu, s0, d);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, d);
-        if (d == 1) s2 += __shfl_xor_sync(0xffffffffu, s2, d);
-      }
-      auto offset = [&](int j, float sum) {
-        // -8 sum in the sums' unit 2^-22, over the constant 2^-14, as two terms
-        const float o = sum * -0.03125f;
-        const uint32_t hi = pack2_f16(o, 0.f), lo = pack2_f16(o - f32x2_of_f16x2(hi).x, 0.f);
-        const int col = j * N + row;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + kQOffset + col * 32 + (((col >> 2) & 1) << 4)), "r"(hi | (lo << 16))
-                     : "memory");
-      };
-      if (r == 0) offset(0, s0);
-      if (r == 1) offset(1, s1);
-      if ((r & 1) == 0) offset(2 + (r >> 1), s2);
-    }
+    const float amax = int4_query_operand<N, kWork, kQChunk>(
+        p.q + ((long(s) * p.q_total + p.q_first) * kHq + g * G) * kDqk, rows, G == 16 ? 4 : 3, sbase, threadIdx.x, cs, [&]() {
+          const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_total + p.q_first;
+          for (int i = threadIdx.x; i < p.q_len * kHalf; i += kWork)
+            rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
+          if (threadIdx.x < N) {
+            // a row that attended nothing (or whose log-sum-exp is no number) adds nothing, nor does a padding column
+            float l = INFINITY;
+            if (threadIdx.x < rows) {
+              l = p.lse[(long(s) * p.q_total + p.q_first + threadIdx.x / G) * kHq + g * G + threadIdx.x % G];
+              l = fabsf(l) < INFINITY ? l * kLog2e : INFINITY;
+            }
+            lse2[threadIdx.x] = -l;  // (added to the logits)
+          }
+          all_sync();
+        });
     if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
     fence_proxy_async_smem();
     all_sync();
@@ -401,18 +297,28 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
         if (good) good = wait_w(done(h), x & 1);
         if (good) {
           tc_fence_after();
+          constexpr int kC = NC % 16 ? 8 : 16;  // columns at a time
 #pragma unroll
-          for (int j = kPer * h; j < kPer * (h + 1); ++j) {
-            uint32_t d[NC];
-            const uint32_t at = t_lane + kColD + j * N + hw * NC;
-            cols_load<NC>(at, d);
-            const float2 zz = f32x2_of_f16x2(z[j >> 1]);
-            const float sc = (j & 1) ? zz.y : zz.x;
-            const uint64_t s2 = pack_f32x2(sc, sc);
-            cols_wait<NC>(d);
+          for (int c0 = 0; c0 < NC; c0 += kC) {
+            uint32_t d[kPer][kC];
 #pragma unroll
-            for (int i = 0; i < NC / 2; ++i)
-              S[i] = fma_f32x2(pack_f32x2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), s2, S[i]);
+            for (int j = 0; j < kPer; ++j) {
+              const uint32_t at = t_lane + kColD + (kPer * h + j) * N + hw * NC + c0;
+              if constexpr (kC == 16) tmem_ld16(at, d[j]);
+              else tmem_ld8(at, d[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              if (j > 0) tied<kC>(d[j]);  // (one wait is for all)
+              else if constexpr (kC == 16) tmem_wait_ld_r16(d[j]);
+              else tmem_wait_ld_r8(d[j]);
+              const float2 zz = f32x2_of_f16x2(z[(kPer * h + j) >> 1]);
+              const float sc = ((kPer * h + j) & 1) ? zz.y : zz.x;
+              const uint64_t s2 = pack_f32x2(sc, sc);
+#pragma unroll
+              for (int i = 0; i < kC / 2; ++i)
+                S[c0 / 2 + i] = fma_f32x2(pack_f32x2(__uint_as_float(d[j][2 * i]), __uint_as_float(d[j][2 * i + 1])), s2, S[c0 / 2 + i]);
+            }
           }
           if (c.t + 1 < t_end) {
             if (h == 0) {
