@@ -37,15 +37,15 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // passes it by more than this many powers of two.
 constexpr float kSlack = 6.f;
 constexpr int kCombineWarps = 4;
+constexpr int kT = 2, kW = 4 * kT, kN = 32 * kW;  // threads a key, warps and threads of a stream
 
 // What depends on the number of columns.
 template <int N>
 struct Lay {
-  // streams, threads a key, warps and threads of a stream
-  static constexpr int kStreams = N == 16 ? 2 : 1, kT = 4 / kStreams, kW = 4 * kT, kN = 32 * kW;
+  static constexpr int kStreams = N == 16 ? 2 : 1;
   static constexpr int kThreads = kStreams * kN + 128;  // and a warpgroup whose first warps issue
   // registers at launch, of a thread that computes and of one that issues
-  static constexpr int kRegs = 96, kRegsWork = 104, kRegsIssue = 64;
+  static constexpr int kRegs = kStreams == 2 ? 96 : 168, kRegsWork = kStreams == 2 ? 104 : 208, kRegsIssue = kStreams == 2 ? 64 : 88;
   static_assert(kStreams * kN * kRegsWork + 128 * kRegsIssue <= kThreads * kRegs, "register split");
   // A tile's logits run in parts of kPer groups, in one where their columns all fit (kSep), else the
   // parts take turns in the same columns.
@@ -150,15 +150,15 @@ __device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
 template <int N>
 __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const __grid_constant__ Decode4Params p) {
   using Y = Lay<N>;
-  constexpr int kT = Y::kT, NC = N / kT, kParts = Y::kParts, kPer = Y::kPer;
+  constexpr int NC = N / kT, kParts = Y::kParts, kPer = Y::kPer;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool issuer = warp >= Y::kStreams * Y::kW;
-  const int str = __shfl_sync(0xffffffffu, issuer ? warp - Y::kStreams * Y::kW : warp / Y::kW, 0);
+  const bool issuer = warp >= Y::kStreams * kW;
+  const int str = __shfl_sync(0xffffffffu, issuer ? warp - Y::kStreams * kW : warp / kW, 0);
   const int gq = warp & 3, hw = (warp >> 2) & (kT - 1);  // the quarter of the tile's keys, and which of a key's threads
-  const int tid = threadIdx.x & (Y::kN - 1);                 // within the stream
+  const int tid = threadIdx.x & (kN - 1);                 // within the stream
   const uint32_t base = sbase + str * Y::kStream;
   const uint32_t vt = base + Y::kOffV, pt = base + Y::kOffP;
   const uint32_t ring_k = base + Y::kOffRingK, ring_v = base + Y::kOffRingV;
@@ -181,12 +181,12 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     for (int i = 0; i < Y::kStagesK; ++i) mbar_init(full_k(i), 1);
     for (int i = 0; i < Y::kStagesV; ++i) mbar_init(full_v(i), 1);
     for (int h = 0; h < kParts; ++h) {
-      mbar_init(ready(h), Y::kW);
+      mbar_init(ready(h), kW);
       mbar_init(done(h), 1);
     }
-    mbar_init(pv_ready, Y::kW);
+    mbar_init(pv_ready, kW);
     mbar_init(pv_done, 1);
-    mbar_init(vote, Y::kW);
+    mbar_init(vote, kW);
     flag[0] = flag[1] = 0;
     if (str == 0) *abort_flag = 0;
     fence_mbar_init();
@@ -362,14 +362,14 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
 
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Y::kRegsWork));
   const uint32_t t_lane = tmem + (uint32_t(gq * 32) << 16);
-  auto stream_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(str + 1), "n"(Y::kN) : "memory"); };
+  auto stream_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(str + 1), "n"(kN) : "memory"); };
   // A barrier that tells whether any thread of the stream brought `v`.
   auto any_of = [&](bool v) -> bool {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(uint32_t(v)), "r"(str + 1), "n"(Y::kN)
+        : "r"(uint32_t(v)), "r"(str + 1), "n"(kN)
         : "memory");
     return r != 0;
   };
@@ -381,18 +381,14 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     tmem_wait_st();
   }
   const int row = gq * 32 + lane;  // this thread's key of the tile
-  const uint32_t v_row = vt + row * 128 + ((row & 7) << 4);
-  constexpr int kQ = 4 / kT;  // words of a thread per group
-  uint32_t W[6 * kQ], zs[3];           // this thread's part of the next tile's key: word 4 j + kQ hw + q of group j at 6 q + j; its scales
+  const uint32_t v_row = vt + hw * Y::kVChunk + row * 128 + ((row & 7) << 4);
+  uint32_t W[12], zs[3];           // this thread's half of the next tile's key: word 4 j + 2 hw + q of group j at 6 q + j; its scales
   int kst = 0, kph = 0, vst = 0, vph = 0;
   auto fetch = [&]() -> bool {
     if (!wait_w(full_k(kst), kph & 1)) return false;
-    const uint32_t at = ring_k + kst * kKBytes, ka = at + row * kI4KCodes + 24 * kQ * hw;
+    const uint32_t at = ring_k + kst * kKBytes, ka = at + row * kI4KCodes + 48 * hw;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if constexpr (kQ == 2) lds128(ka + 16 * i, W + 4 * i);
-      else lds64(ka + 8 * i, W + 2 * i);
-    }
+    for (int i = 0; i < 3; ++i) lds128(ka + 16 * i, W + 4 * i);
 #pragma unroll
     for (int i = 0; i < 3; ++i) zs[i] = lds32(at + kOffKs + row * 2 * kI4KGroups + 4 * i);
     if (++kst == Y::kStagesK) kst = 0, ++kph;
@@ -402,17 +398,16 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
   auto unpack = [&](int h) {
 #pragma unroll
     for (int j = kPer * h; j < kPer * h + kPer; ++j) {
-      uint32_t r[4 * kQ];
+      uint32_t r[8];
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) {
+      for (int q = 0; q < 2; ++q) {
         const uint32_t x = W[6 * q + j], y = x >> 8;
         r[4 * q] = x & kI4Lo;
         r[4 * q + 1] = x & kI4Hi;
         r[4 * q + 2] = y & kI4Lo;
         r[4 * q + 3] = y & kI4Hi;
       }
-      if constexpr (kQ == 2) tmem_st8(t_lane + Y::kColA + 16 * j + 8 * hw, r);
-      else tmem_st4(t_lane + Y::kColA + 16 * j + 4 * hw, r);
+      tmem_st8(t_lane + Y::kColA + 16 * j + 8 * hw, r);
     }
     tmem_wait_st();
   };
@@ -436,11 +431,11 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     const Span U = span_of(p, ctx);
     const int first_pos = ctx - p.q_len;  // slot of the first draft
     // ---- the unit's query operand
-    const float amax = int4_query_operand<N, Y::kN, Y::kQChunk>(
+    const float amax = int4_query_operand<N, kN, Y::kQChunk>(
         p.q + (long(s) * p.q_len * kHq + g * G) * kDqk, rows, g_log, base, tid, cs, [&]() {
           stream_sync();  // (the unit before has read what is written here)
           const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
-          for (int i = tid; i < p.q_len * kHalf; i += Y::kN)
+          for (int i = tid; i < p.q_len * kHalf; i += kN)
             rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
           if (tid < N) nref[tid] = tid < rows ? INFINITY : -INFINITY;  // (a padding column: weight 0)
           stream_sync();
@@ -542,7 +537,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         if (raise) flag[x & 1] = x + 1;
         mbar_arrive(vote);
       }
-      // ---- values: (code - 8) * scale in fp16, this thread's groups.  1024 + n and 64 + n come out of a
+      // ---- values: (code - 8) * scale in fp16, this thread's 64 dims.  1024 + n and 64 + n come out of a
       // word with one LOP3; the scale is not folded into the weights, as a row of 64 dims has two.
       // A slot nothing was written to may hold any scale: it counts as 0
       // (where the logits run in parts, the last one's sums stand after the product of the tile before)
@@ -550,12 +545,13 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
       if (good) good = wait_w(full_v(vst), vph & 1);
       if (good) {
         const uint32_t at = ring_v + vst * kVBytes;
+        uint32_t sv = lds32(at + kOffVs + row * 2 * kI4VGroups + 4 * hw);
+        sv = key <= U.hi ? sv : 0u;
 #pragma unroll
-        for (int u = 0; u < kQ; ++u) {
-          const int j = hw * kQ + u;  // group
-          const uint32_t sv = key <= U.hi ? lds16(at + kOffVs + row * 2 * kI4VGroups + 2 * j) : 0u, s2 = sv | (sv << 16);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t s2 = __byte_perm(sv, 0, u ? 0x3232 : 0x1010);
           uint32_t vw[4];
-          lds128(at + row * kI4VCodes + ((j ^ ((row >> 1) & 3)) << 4), vw);
+          lds128(at + row * kI4VCodes + (((2 * hw + u) ^ ((row >> 1) & 3)) << 4), vw);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t y = vw[i] >> 8;
@@ -564,7 +560,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
             o[1] = hmul2(hadd2(field(vw[i], kI4Hi, k64), 0xD480D480u), s2);    // - 72
             o[2] = hmul2(hadd2(field(y, kI4Lo, k1024), 0xE408E408u), s2);
             o[3] = hmul2(hadd2(field(y, kI4Hi, k64), 0xD480D480u), s2);
-            sts128((v_row ^ ((4 * (j & 1) + i) << 4)) + (j >> 1) * Y::kVChunk, o);
+            sts128(v_row ^ ((4 * u + i) << 4), o);
           }
         }
       }
@@ -727,6 +723,7 @@ cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s) {
   const int rows = p.q_len * p.group;
   if (rows <= 16) return launch_n<16>(p, sms, s);
   if (rows <= 32) return launch_n<32>(p, sms, s);
+  if (rows <= 48) return launch_n<48>(p, sms, s);
   if (rows <= 64) return launch_n<64>(p, sms, s);
   if (rows <= 96) return launch_n<96>(p, sms, s);
   return launch_n<128>(p, sms, s);
