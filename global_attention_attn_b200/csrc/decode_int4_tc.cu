@@ -45,7 +45,7 @@ struct Lay {
   static constexpr int kStreams = N == 16 ? 2 : 1;
   static constexpr int kThreads = kStreams * kN + 128;  // and a warpgroup whose first warps issue
   // registers at launch, of a thread that computes and of one that issues
-  static constexpr int kRegs = kStreams == 2 ? 96 : 168, kRegsWork = kStreams == 2 ? 104 : 208, kRegsIssue = kStreams == 2 ? 64 : 88;
+  static constexpr int kRegs = kStreams == 2 ? 96 : 168, kRegsWork = kStreams == 2 ? kRegs : 208, kRegsIssue = kStreams == 2 ? kRegs : 88;
   static_assert(kStreams * kN * kRegsWork + 128 * kRegsIssue <= kThreads * kRegs, "register split");
   // A tile's logits run in parts of kPer groups, in one where their columns all fit (kSep), else the
   // parts take turns in the same columns.
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
   };
 
   if (issuer) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Y::kRegsIssue));
+    if constexpr (Y::kRegsIssue != Y::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Y::kRegsIssue));
     if (n_all > 0) {
       // ---- copies of the piece's tiles in order, and each tile's products.  A slot of keys is free
       // when the last part of its logits may run, one of values when its product may.
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     return;
   }
 
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Y::kRegsWork));
+  if constexpr (Y::kRegsWork != Y::kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Y::kRegsWork));
   const uint32_t t_lane = tmem + (uint32_t(gq * 32) << 16);
   auto stream_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(str + 1), "n"(kN) : "memory"); };
   // A barrier that tells whether any thread of the stream brought `v`.
