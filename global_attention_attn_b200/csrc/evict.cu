@@ -23,6 +23,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 constexpr uint32_t kZeroKey = 0x80000000u, kKeepKey = 0xFFFFFFFFu;
 
+// Whether a key tells its score's bits (not -0 or 0, NaN or -infinity, a slot kept whatever it scores), and those.
+__device__ __forceinline__ bool exact_key(uint32_t k) { return k != kZeroKey && k != kKeepKey && k > 0x007FFFFFu; }
+__device__ __forceinline__ float key_score(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;  // 11, 11 and 10 bits a pass
 static_assert(kBins == 4 * kSelThreads, "a thread's bins are one 16-byte read");
@@ -61,10 +68,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   __shared__ uint32_t part[2];      // this CTA's counts, for the CTAs behind it
   cg::cluster_group cl = cg::this_cluster();
   const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
-  auto sync = [&]() {
-    if (C == 1) __syncthreads();
-    else cl.sync();
-  };
   const int row = blockIdx.x / C, s = row / p.hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int L = p.seq_lens[s];
   if (L < 0 || L > p.max_seq_len) {
@@ -73,6 +76,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   }
 #pragma unroll
   for (int i = 0; i < 3; ++i) reinterpret_cast<uint4*>(hist[i])[tid] = make_uint4(0, 0, 0, 0);
+  if (C > 1) cluster_arrive();
   const float* const src = p.scores + long(row) * p.score_stride;
   const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
   const int per = ((L + C - 1) / C + 127) & ~127;  // slots of a CTA
@@ -141,7 +145,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   int need = p.keep;
   uint32_t prefix = 0, mask = 0;  // keys & mask == prefix are still in question
   bool whole = all;               // every slot whose key matches the prefix stays
-  __syncthreads();
+  if (C > 1) cluster_wait();      // every CTA's bins are 0
+  else __syncthreads();
   for (int pass = 0; !whole && pass < 3; ++pass) {  // (cluster-uniform: all of this is the row's)
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
     uint32_t* const hs = hist[pass];
@@ -152,17 +157,23 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
         if ((key[e] & mask) == prefix && key[e] != kZeroKey) atomicAdd(hs + ((key[e] >> shift) & low), 1u);
     });
     if (lane == 0 && zeros && (kZeroKey & mask) == prefix) atomicAdd(hs + ((kZeroKey >> shift) & low), zeros);
-    sync();
-    // bins from the largest down, 4 a thread, summed over the cluster
-    uint32_t h[4] = {0, 0, 0, 0};
-#pragma unroll 8
-    for (int r = 0; r < C; ++r) {
-      const uint4 v = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hs, r) + kBins - 4 - 4 * tid);
-      h[0] += v.w;
-      h[1] += v.z;
-      h[2] += v.y;
-      h[3] += v.x;
+    // the cluster's bins add up in one CTA's: few of a CTA's bins hold anything
+    const int leader = pass % C;
+    __syncthreads();
+    if (C > 1) {
+      if (rank != leader) {
+        uint32_t* const to = cl.map_shared_rank(hs, leader);
+        const uint4 v = reinterpret_cast<const uint4*>(hs)[tid];
+        const uint32_t mine[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (mine[e]) atomicAdd(to + 4 * tid + e, mine[e]);
+      }
+      cl.sync();
     }
+    // bins from the largest down, 4 a thread
+    const uint4 b4 = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hs, leader) + kBins - 4 - 4 * tid);
+    const uint32_t h[4] = {b4.w, b4.z, b4.y, b4.x};
     const uint32_t sum = h[0] + h[1] + h[2] + h[3];
     uint32_t incl = sum;
 #pragma unroll
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
           const uint32_t j = mo + min(ti, take);
           const int slot = at0 + 128 * k + e;
           idx[j] = slot;
-          if (out) out[j] = __ldg(src + slot);
+          if (out) out[j] = exact_key(key[e]) ? key_score(key[e]) : __ldg(src + slot);
         }
         mo += up;
         ti += eq;
