@@ -13,11 +13,30 @@
 //   - O^T = V^T P^T: a thread unpacks half of its key's value row to fp16, scale applied, into
 //     shared memory ([key][dim], the M-major operand), and stores its weights beside it.  The
 //     sums of all tiles stay in tensor memory, 128 dims x columns.
-// A column is a query row of the KV head (draft, head).  Its reference is common to the tile's
-// warps (they share the sums): they meet at one barrier per tile, where a logit that has passed
-// the reference by 2^6 makes all of them move it; else nothing is rescaled.
-// Eight warps (two threads a key) work on a tile, a ninth issues copies and products.  One token of
-// a KV head is 16 columns: its tensor memory allows two such streams per SM, more columns one.
+// A column is a query row of the KV head (draft, head).  Its reference is common to a tile's warps,
+// which share the sums: after its logits a warp tells the others whether one has passed the
+// reference by 2^6, and reads their answer after the values are unpacked; only then do all of
+// them meet and move it, else nothing is rescaled.
+//
+// Eight warps (two threads a key) work on a tile, another issues copies and products.  One token
+// of a KV head is 16 columns, whose tensor and shared memory let two such streams share an SM; more
+// columns have one stream.  (Four threads a key: 4 and 8 drafts 103 and 215 us against 97 and 195
+// below, the work that does not divide by columns done twice.)  From 64 columns on the six group
+// sums do not fit beside the output's, so the logits run in two or three parts that take turns in
+// the same columns; an SM's warps hide the wait between them with the next tile's keys.
+// Workers are the streams: the tiles of all sequences and KV heads form one line, cut into as many
+// equal pieces as there are workers, so any mix of lengths loads every SM alike.  A piece's first
+// and last (sequence, head) may be partial and go through the combine kernel, the others write
+// their rows directly; contexts of up to 256 keys are cut between units only.
+//
+// Measured (graph replay, in brackets the same on mma.sync with the drafts' rows in warps of their
+// own): 64 sequences of 4096..65536 keys, one token, 430 us (548), 3.6 TB/s, 0.55 of a copy's rate;
+// one of 131001 keys 41 us (64); one of 500 12.4 us (18.5); 16 of 1001..16384 with 1, 2, 4, 8
+// drafts 45, 64, 97 (160), 195 us.  Bound by the warps' instructions, 540 per warp and tile of
+// 16 columns (half of them the unpacking): without its copies' arithmetic the first call takes
+// 260 us.  Short calls are the sum of what a worker does once: 2 us to its first tile's copy,
+// 1.5 us for the query operand, 3 us for the first tile (nothing overlaps yet, the references are
+// set) and 1.5 us for its rows.
 #include "int4_tc.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
@@ -37,7 +56,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // passes it by more than this many powers of two.
 constexpr float kSlack = 6.f;
 constexpr int kCombineWarps = 4;
-constexpr int kT = 2, kW = 4 * kT, kN = 32 * kW;  // threads a key, warps and threads of a stream
+constexpr int kW = 8, kN = 32 * kW;  // warps and threads of a stream, two threads a key
 
 // What depends on the number of columns.
 template <int N>
@@ -150,14 +169,14 @@ __device__ __forceinline__ Span span_of(const Decode4Params& p, int ctx) {
 template <int N>
 __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const __grid_constant__ Decode4Params p) {
   using Y = Lay<N>;
-  constexpr int NC = N / kT, kParts = Y::kParts, kPer = Y::kPer;
+  constexpr int NC = N / 2, kParts = Y::kParts, kPer = Y::kPer;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool issuer = warp >= Y::kStreams * kW;
   const int str = __shfl_sync(0xffffffffu, issuer ? warp - Y::kStreams * kW : warp / kW, 0);
-  const int gq = warp & 3, hw = (warp >> 2) & (kT - 1);  // the quarter of the tile's keys, and which of a key's threads
+  const int gq = warp & 3, hw = (warp >> 2) & 1;  // the quarter of the tile's keys, and which of a key's two threads
   const int tid = threadIdx.x & (kN - 1);                 // within the stream
   const uint32_t base = sbase + str * Y::kStream;
   const uint32_t vt = base + Y::kOffV, pt = base + Y::kOffP;

@@ -53,9 +53,11 @@ __device__ __forceinline__ uint2 warps_before(uint32_t* buf, uint32_t mine, int 
 // One cluster per (sequence, KV head) row.  The row is read once (4 bytes a slot, the floor) by the
 // cluster's 1..8 CTAs, and stays with them: 4 Q keys a thread in registers, or in shared memory
 // for the longest rows.  A lane takes 4 neighbouring slots at a step, a warp 128, so that order
-// costs one scan per 128 slots.  The border is found by up to three histogram passes (bins
-// summed over the cluster through distributed shared memory, every CTA drawing the same
-// conclusion; a pass whose bin is wanted whole is the last), then each CTA writes its part of
+// costs one scan per 128 slots.  The border is found by up to three histogram passes (a CTA adds
+// its bins that hold anything to those of one of the cluster through distributed shared memory,
+// and every CTA draws the same conclusion from these: 56 us for 16 sequences of 40000..131072
+// slots and 4 heads, against 65 with every CTA reading the bins of all; a pass whose bin is wanted
+// whole is the last), then each CTA writes its part of
 // the kept slots at the place that the counts of the parts before it give: ascending, equal
 // scores lowest slot first.  Slots never attended all score 0, so zeros are counted aside and
 // enter the histogram once per warp; other equal scores add up one by one.

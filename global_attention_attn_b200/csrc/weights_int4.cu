@@ -2,20 +2,20 @@
 //
 // On mma.sync this operator is bound by the products: 17 steps of 16 x 8 x 16 per 16 keys and
 // draft, at 8.9 cycles of a scheduler each, and the keys unpacked again for every draft (235 us
-// for 8 sequences of 4099..65536 keys and 4 drafts, 130 MB).  A tcgen05.mma of 128 keys costs
-// about 56 cycles for any number of columns up to 64, so all drafts of a KV head (up to 64 rows:
-// 4 drafts of 16 heads, 8 of 8) are one product's columns, and a key is unpacked once.
+// for 8 sequences of 4099..65536 keys and 4 drafts, 130 MB).  A tcgen05.mma of 128 keys and 64
+// columns costs 34 cycles of a unit of its own, so all drafts of a KV head (up to 64 rows: 4
+// drafts of 16 heads, 8 of 8) are one product's columns, and a key is unpacked once: 88 us, and
+// 60 us with one token.
 //
 // One CTA per SM takes a contiguous piece of the line of 128-key tiles (a tile is a page).  Two
 // threads share a key: they unpack half of its words each into the A operand in tensor memory,
 // and each applies the key's 6 scales to its half of the columns' 6 group sums and adds up the
-// exponentials; one of the two updates the score.  (Four threads a key: 105 us for the call above
-// against 99.)  The tensor memory is 96 columns of keys, 8 of a constant (the code offset's
-// factor, decode_int4_tc.cu) and 6 x 64 of sums, all single: groups 0..2 and 3..5 run as two
-// parts, so that the products of one run behind the arithmetic on the other (three parts 109 us,
-// six 141: what bounds the kernel is instructions and the parts' handshakes, not the products;
-// with neither products nor reads of the sums it takes 88).  A ninth warp issues copies and
-// products.
+// exponentials; one of the two updates the score.  (Four threads a key: 98 us for the call above.)
+// The tensor memory is 96 columns of keys, 8 of a constant (the code offset's factor) and 6 x 64
+// of sums, all single: groups 0..2 and 3..5 run as two parts, so that the products of one run
+// behind the arithmetic on the other (three parts were a tenth slower, six two fifths).  What
+// bounds the kernel is instructions and the parts' handshakes, not the products and not the
+// copies (1.5 TB/s).  A ninth warp issues copies and products.
 #include "int4_tc.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
