@@ -55,7 +55,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Weights are 2^(z - ref): ref is a column's maximum when it was set, and moves only when a logit
 // passes it by more than this many powers of two.
 constexpr float kSlack = 6.f;
-constexpr int kCombineWarps = 4;
 constexpr int kW = 8, kN = 32 * kW;  // warps and threads of a stream, two threads a key
 
 // What depends on the number of columns.
@@ -748,14 +747,16 @@ cudaError_t launch_decode4_tc(const Decode4Params& p, int sms, cudaStream_t s) {
   return launch_n<128>(p, sms, s);
 }
 
-// One block per (query row, head): merges the pieces that share the row's unit.  A long context
-// of a small batch has hundreds, each a dependent load away: the warps take every fourth, and
-// the first warp adds up the warps' sums (a fixed order, whatever the timing).
-__global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
-  __shared__ float4 part[kCombineWarps][32];
-  __shared__ float part_m[kCombineWarps], part_l[kCombineWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qrow = blockIdx.x / kHq, h = blockIdx.x % kHq, s = qrow / p.q_len, g = h / p.group;
+// Merges the pieces that share a (query row, head)'s unit, kRow warps a row: a long context of a
+// small batch has hundreds, each a dependent load away, so the warps take turns and the first adds
+// up their sums (a fixed order, whatever the timing).
+template <int kRow>
+__global__ void __launch_bounds__(kRow == 1 ? 128 : 32 * kRow) decode4_combine_kernel(const __grid_constant__ Decode4Params p) {
+  __shared__ float4 part[kRow][32];
+  __shared__ float part_m[kRow], part_l[kRow];
+  const int lane = threadIdx.x & 31, warp = kRow == 1 ? 0 : threadIdx.x >> 5;
+  const int at = kRow == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int qrow = at / kHq, h = at % kHq, s = qrow / p.q_len, g = h / p.group;
   pdl_wait_prerequisites();  // (the pieces stand from here on)
   const long long total = p.ws_tbl[p.batch] * p.hkv;
   const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
@@ -770,13 +771,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
   auto piece = [&](int i) { return (i == 0 ? first : 2L * (w0 + i)) * rows + rr; };
   const int n = w1 - w0 + 1;
   float M = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kCombineWarps * 32) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
+  for (int i = 32 * warp + lane; i < n; i += 32 * kRow) M = fmaxf(M, p.ws_ml[2 * piece(i)]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if (lane == 0) part_m[warp] = M;
-  __syncthreads();
+  if constexpr (kRow > 1) {
+    if (lane == 0) part_m[warp] = M;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kCombineWarps; ++i) M = fmaxf(M, part_m[i]);
+    for (int i = 0; i < kRow; ++i) M = fmaxf(M, part_m[i]);
+  }
   float sl = -INFINITY;
   if (p.sink) {
     sl = p.sink[h] * kLog2e;
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = warp; i < n; i += kCombineWarps) {
+  for (int i = warp; i < n; i += kRow) {
     const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * piece(i));
     const float f = ex2(ml.x - M);
     const float4 v = *reinterpret_cast<const float4*>(p.ws_o + piece(i) * kDv + lane * 4);
@@ -795,18 +798,20 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
     acc.z += f * v.z;
     acc.w += f * v.w;
   }
-  part[warp][lane] = acc;
-  if (lane == 0) part_l[warp] = L;
-  __syncthreads();
-  if (warp > 0) return;
+  if constexpr (kRow > 1) {
+    part[warp][lane] = acc;
+    if (lane == 0) part_l[warp] = L;
+    __syncthreads();
+    if (warp > 0) return;
 #pragma unroll
-  for (int i = 1; i < kCombineWarps; ++i) {
-    const float4 v = part[i][lane];
-    L += part_l[i];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+    for (int i = 1; i < kRow; ++i) {
+      const float4 v = part[i][lane];
+      L += part_l[i];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
   }
   if (p.sink) L += ex2(sl - M);
   const float sc = p.v_scale / L;
@@ -815,20 +820,21 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode4_combine_kernel(con
   if (p.lse && lane == 0) p.lse[long(qrow) * kHq + h] = (M + log2f(L)) * kLn2;
 }
 
-
 // Launched with programmatic serialization: its launch overlaps the decode's last blocks (131001 keys of one
 // sequence 42.5 -> 41.4 us; waiting on the SMs from the decode's start on it cost 45.3).
 cudaError_t launch_decode4_combine(const Decode4Params& p, cudaStream_t s) {
+  const int rows = p.batch * p.q_len * kHq, pieces = p.workers / (p.batch * p.hkv) + 1;  // a unit's, about
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.batch * p.q_len * kHq));
-  cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode4_combine_kernel, p);
+  cfg.gridDim = dim3(unsigned(pieces <= 4 ? rows / 4 : rows));
+  cfg.blockDim = dim3(pieces <= 16 ? 128 : 512);
+  auto kernel = pieces <= 4 ? decode4_combine_kernel<1> : (pieces <= 16 ? decode4_combine_kernel<4> : decode4_combine_kernel<16>);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace mimo
