@@ -540,13 +540,20 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         return key > min(at, U.hi) || (p.window > 0 && key <= at - p.window);
       };
       float top = -INFINITY;
+      // where registers allow, the weights are made here, in the hope that no reference moves
+      constexpr bool kEarly = NC <= 16;
+      float ws[kEarly ? NC : 8];
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i) {
-        float xs[8], t8 = -INFINITY;
+        float* const xs = ws + (kEarly ? 8 * i : 0);
+        float t8 = -INFINITY;
         logits(i, xs);
+        if (edge && hidden(i)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xs[e] = -INFINITY;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) t8 = fmaxf(t8, xs[e]);
-        if (edge && hidden(i)) t8 = -INFINITY;
         top = fmaxf(top, t8);
       }
       // (the warps tell each other which tile moves the references; the answer is read after the values)
@@ -555,6 +562,18 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         if (raise) flag[x & 1] = x + 1;
         mbar_arrive(vote);
       }
+      auto weights = [&](int i, float* xs) {
+        logits(i, xs);
+        if (edge && hidden(i)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xs[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xs[e] = ex2(xs[e]);
+      };
+      if constexpr (kEarly)
+#pragma unroll
+        for (int e = 0; e < NC; ++e) ws[e] = ex2(ws[e]);
       // ---- values: (code - 8) * scale in fp16, this thread's 64 dims.  1024 + n and 64 + n come out of a
       // word with one LOP3; the scale is not folded into the weights, as a row of 64 dims has two.
       // A slot nothing was written to may hold any scale: it counts as 0
@@ -624,18 +643,15 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
           }
           tmem_wait_st();
         }
+        if constexpr (kEarly)
+#pragma unroll
+          for (int i = 0; i < NC / 8; ++i) weights(i, ws + 8 * i);
       }
       // ---- weights
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i) {
-        float xs[8];
-        logits(i, xs);
-        if (edge && hidden(i)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) xs[e] = -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xs[e] = ex2(xs[e]);
+        float* const xs = ws + (kEarly ? 8 * i : 0);
+        if constexpr (!kEarly) weights(i, xs);
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
