@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
       };
       float top = -INFINITY;
       // where registers allow, the weights are made here, in the hope that no reference moves
-      constexpr bool kEarly = NC <= 16;
+      constexpr bool kEarly = NC <= 32;
       float ws[kEarly ? NC : 8];
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i) {
