@@ -171,9 +171,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, t):
+    """Handle of the stream that a call on tensor t goes to."""
     if stream is None:
         import torch
+        if t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {t.device}, which is not the current device")
         # (the handle alone: making a torch.cuda.Stream of it takes 3 us, a quarter of a short decode)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -249,9 +252,9 @@ def mimo_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, *, num_kv_heads: int,
     a.ev_kernel_begin, a.ev_kernel_end = _events(kernel_events)
     a.ring_slots = int(ring_slots)
     if stall_test_wait_ns is not None:
-        _check(lib().mimo_attn_prefill_stall_test(C.byref(a), _stream(stream), int(stall_test_wait_ns)))
+        _check(lib().mimo_attn_prefill_stall_test(C.byref(a), _stream(stream, q), int(stall_test_wait_ns)))
     else:
-        _check(lib().mimo_attn_prefill(C.byref(a), _stream(stream)))
+        _check(lib().mimo_attn_prefill(C.byref(a), _stream(stream, q)))
     return out, lse
 
 
@@ -295,7 +298,7 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
     a.ring_slots, a.q_len = int(ring_slots), int(q_len)
     a.positions = _ptr(positions)
-    _check(lib().mimo_attn_decode(C.byref(a), _stream(stream)))
+    _check(lib().mimo_attn_decode(C.byref(a), _stream(stream, q)))
     return out, lse
 
 
@@ -317,7 +320,7 @@ def mimo_attn_decode_noalloc(q, seq_lens, *, max_seq_len: int, num_kv_heads: int
     a.out, a.lse = _ptr(out), _ptr(lse)
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
     a.ring_slots = int(ring_slots)
-    _check(lib().mimo_attn_decode_noalloc(C.byref(a), _stream(stream)))
+    _check(lib().mimo_attn_decode_noalloc(C.byref(a), _stream(stream, q)))
     return out, lse
 
 
@@ -341,7 +344,7 @@ def mimo_kv_append(k_new, v_new, pos, seq_idx, *, rope_base: float, cache_kind: 
     a.num_pages = num_pages
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
     a.ring_slots, a.slots = int(ring_slots), _ptr(slots)
-    _check(lib().mimo_kv_append(C.byref(a), _stream(stream)))
+    _check(lib().mimo_kv_append(C.byref(a), _stream(stream, k_new)))
 
 
 def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_base: float, k_cache,
@@ -353,8 +356,9 @@ def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_head
     if q.shape[0] % q_len:
         raise ValueError("q holds batch * q_len rows")
     B = q.shape[0] // q_len
-    if scores.ndim != 3 or scores.shape[0] != B or scores.shape[1] != num_kv_heads or not scores.is_contiguous():
-        raise ValueError("scores is a contiguous [batch, num_kv_heads, slots] tensor")
+    if (scores.ndim != 3 or scores.shape[0] != B or scores.shape[1] != num_kv_heads or not scores.is_contiguous()
+            or scores.element_size() != 4):
+        raise ValueError("scores is a contiguous float32 [batch, num_kv_heads, slots] tensor")
     a = MimoWeightsArgs()
     a.layer = make_layer(num_kv_heads, rope_base, 0, None, softmax_scale, 1.0)
     a.batch, a.q_len, a.max_seq_len = B, int(q_len), int(max_seq_len)
@@ -363,7 +367,7 @@ def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_head
     a.max_pages, a.num_pages = block_table.shape[1], num_pages
     a.cache_dtype, a.k_dequant = cache_dtype, _ptr(k_dequant)
     a.scores, a.score_stride = _ptr(scores), scores.shape[2]
-    _check(lib().mimo_attn_weights(C.byref(a), _stream(stream)))
+    _check(lib().mimo_attn_weights(C.byref(a), _stream(stream, q)))
     return scores
 
 
@@ -374,9 +378,12 @@ def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int
     [num_seqs, num_kv_heads, slots].  Returns (idx int32 [num_seqs, num_kv_heads, keep] ascending,
     padded with -1; counts int32 [num_seqs]; the kept slots' scores, padded with 0)."""
     import torch
-    if scores.ndim != 3 or not scores.is_contiguous():
-        raise ValueError("scores is a contiguous [num_seqs, num_kv_heads, slots] tensor")
+    if scores.ndim != 3 or not scores.is_contiguous() or scores.element_size() != 4:
+        raise ValueError("scores is a contiguous float32 [num_seqs, num_kv_heads, slots] tensor")
     n, h, slots = scores.shape
+    for t, size, name in ((idx, n * h * keep, "idx"), (counts, n, "counts"), (scores_out, n * h * keep, "scores_out")):
+        if t is not None and (t.numel() != size or t.element_size() != 4 or not t.is_contiguous()):
+            raise ValueError(f"{name} is a contiguous 32-bit tensor of {size} elements")
     if idx is None:
         idx = scores.new_empty((n, h, keep), dtype=torch.int32)
     if counts is None:
@@ -388,7 +395,7 @@ def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int
     a.seq_lens, a.max_seq_len = _ptr(seq_lens), int(max_seq_len)
     a.keep, a.recent, a.first = int(keep), int(recent), int(first)
     a.idx, a.counts, a.scores_out = _ptr(idx), _ptr(counts), _ptr(scores_out)
-    _check(lib().mimo_kv_select(C.byref(a), _stream(stream)))
+    _check(lib().mimo_kv_select(C.byref(a), _stream(stream, scores)))
     return idx, counts, scores_out
 
 
@@ -403,8 +410,9 @@ def mimo_kv_gather(k_src, v_src, block_table_src, k_dst, v_dst, block_table_dst,
     a.num_seqs, a.num_kv_heads = block_table_src.shape[0], num_kv_heads
     if block_table_dst.shape[0] != a.num_seqs or counts.shape[0] != a.num_seqs:
         raise ValueError("both block tables and counts have a row per sequence")
-    if idx is not None and (idx.ndim != 3 or tuple(idx.shape[:2]) != (a.num_seqs, num_kv_heads) or not idx.is_contiguous()):
-        raise ValueError("idx is a contiguous [num_seqs, num_kv_heads, n] tensor")
+    if idx is not None and (idx.ndim != 3 or tuple(idx.shape[:2]) != (a.num_seqs, num_kv_heads) or not idx.is_contiguous()
+                            or idx.element_size() != 4):
+        raise ValueError("idx is a contiguous int32 [num_seqs, num_kv_heads, n] tensor")
     if max_count is None:
         max_count = block_table_dst.shape[1] * 128
         if idx is not None:
@@ -417,7 +425,7 @@ def mimo_kv_gather(k_src, v_src, block_table_src, k_dst, v_dst, block_table_dst,
     a.max_count = int(max_count)
     a.cache_dtype, a.out_dtype = cache_dtype, cache_dtype if out_dtype is None else out_dtype
     a.k_dequant, a.v_dequant = _ptr(k_dequant), _ptr(v_dequant)
-    _check(lib().mimo_kv_gather(C.byref(a), _stream(stream)))
+    _check(lib().mimo_kv_gather(C.byref(a), _stream(stream, k_src)))
 
 
 def empty_int4_cache(blocks: int, num_kv_heads: int, ring_slots: int = 0, device="cuda"):

@@ -246,7 +246,7 @@ MIMO_API int mimo_attn_prefill_stall_test(const mimo_prefill_args* args, void* s
  * window) on a bf16 paged cache run the tensor-core prefill kernel, whose 128-row tile
  * holds the q_len x 16 query rows of one KV head, over page-aligned splits, then the same
  * combine pass.  Either way the split-KV workspace is the one the size queries give.  4-bit
- * caches (MIMO_DTYPE_INT4) have a decode kernel and a workspace size query of their own
+ * caches (MIMO_DTYPE_INT4) have decode kernels and a workspace size query of their own
  * (mimo_attn_decode_int4_workspace_size); there a seq_lens above max_seq_len is always
  * reported, and its keys from max_seq_len on are not attended.
  *
@@ -296,7 +296,8 @@ MIMO_API size_t mimo_attn_verify_workspace_size(int batch, int q_len, int max_se
                                                 int window);
 
 /* The same for a 4-bit cache (MIMO_DTYPE_INT4) of the given kind; at most 20 MB, whatever the
- * batch.  0 for sizes that a call refuses. */
+ * batch.  0 for sizes that a call refuses.  Calls that may run at the same time (on two streams, in
+ * two graphs) need a workspace each. */
 MIMO_API size_t mimo_attn_decode_int4_workspace_size(int batch, int q_len, int max_seq_len, int num_kv_heads,
                                                      int window, int cache_kind);
 
@@ -448,8 +449,8 @@ MIMO_API int mimo_kv_select(const mimo_select_args* args, void* stream);
  * E4M3 or 4-bit source, is a bf16 cache: the values the codes stand for, rounded once (key
  * dims 0..63 to fp16), as prefill over a stored prefix reads them.  Keys keep the rotation they
  * were appended with: decode passes `positions`, append `slots` afterwards.
- * No page may be both read and written by one call: evict into fresh pages and release the old
- * ones (pages shared between sequences stay whole).  Destination slots from counts[s] on are
+ * No page may be both read and written by one call, nor written for two sequences: evict into fresh
+ * pages and release the old ones (pages shared between sequences stay whole).  Destination slots from counts[s] on are
  * left as they were.  A slot or page outside its table or cache sets MIMO_STATUS_BAD_INDEX and
  * is skipped; counts[s] above max_count is cut to it and reported.
  */

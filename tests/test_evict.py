@@ -77,6 +77,28 @@ def test_gather_refusals(kw):
     assert "mimo_kv_gather" in M.lib().mimo_last_error().decode()
 
 
+def test_python_refusals(monkeypatch):
+    """What the binding can see of a tensor: element sizes, shapes, the device."""
+    s, n = torch.zeros((2, 4, 64)), torch.ones(2, dtype=torch.int32)
+    for bad in (s.half(), s[:, :, ::2], s[0]):
+        with pytest.raises(ValueError, match="scores"):
+            M.mimo_kv_select(bad, n, max_seq_len=32, keep=8, stream=0)
+        with pytest.raises(ValueError, match="scores"):
+            M.mimo_attn_weights(torch.zeros((2, 64, 192), dtype=torch.bfloat16), torch.zeros((2, 64)), bad, n, max_seq_len=32,
+                                num_kv_heads=4, rope_base=1e7, k_cache=s, block_table=n[:, None], num_pages=1, stream=0)
+    for kw in (dict(idx=torch.zeros((2, 4, 7), dtype=torch.int32)), dict(idx=torch.zeros((2, 4, 8), dtype=torch.int64)),
+               dict(counts=torch.zeros(3, dtype=torch.int32)), dict(scores_out=torch.zeros((2, 4, 8), dtype=torch.half))):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            M.mimo_kv_select(s, n, max_seq_len=64, keep=8, stream=0, **kw)
+    with pytest.raises(ValueError, match="idx"):
+        M.mimo_kv_gather(s, s, n[:, None], s, s, n[:, None], n, num_kv_heads=4, num_pages=1, num_pages_out=1,
+                         idx=torch.zeros((2, 4, 8), dtype=torch.int64), stream=0)
+    other = type("T", (), dict(is_cuda=True, device=torch.device("cuda", 1)))()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        M._stream(None, other)
+
+
 def test_unsupported_heads():
     assert _weights(hkv=2) == _select(num_kv_heads=2) == _gather(num_kv_heads=16) == M.MIMO_ERR_UNSUPPORTED
 

@@ -269,6 +269,74 @@ def test_decode_wide_logits_and_max_seq_len():
 
 
 @gpu
+@pytest.mark.parametrize("q_len", [2, 3, 4, 6, 8])
+def test_decode_drafts_wide_logits(q_len):
+    """The references of every number of columns move, with the sums of the tiles before."""
+    check_paged([3000, 700], q_mul=8.0, q_len=q_len, seed=39)
+
+
+@gpu
+def test_decode_drafts_long():
+    check_paged([70001, 300], q_len=4, seed=45)
+
+
+@gpu
+@pytest.mark.parametrize("q_len", [1, 4, 8])
+def test_decode_a_nan_query_row_is_alone(q_len):
+    """A row of NaN: NaN in its output and log-sum-exp, every other row bit for bit as without it."""
+    g, lens = gen(46), [900, 131]
+    table, pages = R.table_of(lens, np.random.default_rng(46))
+    k, v, _, _ = R.random_cache(R.INT4, pages, g)
+    q = torch.randn((2 * q_len, 64, 192), generator=g, device="cuda").bfloat16()
+    run = lambda x: M.mimo_attn_decode(x, R.i32(lens), max_seq_len=900, num_kv_heads=4, rope_base=1e7, window=0,
+                                       cache_kind=PAGED, k_cache=k, v_cache=v, block_table=table, num_pages=pages,
+                                       cache_dtype=M.MIMO_DTYPE_INT4, q_len=q_len)
+    o1, l1 = run(q)
+    bad = q.clone()
+    bad[q_len, 37] = float("nan")
+    o2, l2 = run(bad)
+    assert torch.isnan(o2[q_len, 37]).all() and torch.isnan(l2[q_len, 37])
+    o2[q_len, 37], l2[q_len, 37] = o1[q_len, 37], l1[q_len, 37]
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    M.status_poll()
+
+
+@gpu
+def test_decode_two_streams_and_two_graphs_at_once():
+    """Calls that run at the same time, each with its workspace: the results of the calls alone."""
+    g = gen(47)
+    sets = []
+    for i, lens in enumerate(([30000], [20000, 7, 4000])):
+        table, pages = R.table_of(lens, np.random.default_rng(47 + i))
+        k, v, _, _ = R.random_cache(R.INT4, pages, g)
+        q = torch.randn((len(lens), 64, 192), generator=g, device="cuda").bfloat16()
+        kw = dict(max_seq_len=max(lens), num_kv_heads=4, rope_base=1e7, window=0, cache_kind=PAGED, k_cache=k, v_cache=v,
+                  block_table=table, num_pages=pages, cache_dtype=M.MIMO_DTYPE_INT4)
+        sets.append((q, R.i32(lens), kw, M.mimo_attn_decode(q, R.i32(lens), **kw)))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], []
+    for _ in range(3):
+        for st, (q, lens, kw, _r) in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append((M.mimo_attn_decode(q, lens, **kw), _r))
+    torch.cuda.synchronize()
+    graphs = []
+    for q, lens, kw, ref in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            r = M.mimo_attn_decode(q, lens, **kw)
+        graphs.append((graph, r, ref))
+    for st, (graph, r, ref) in zip(streams, graphs):
+        with torch.cuda.stream(st):
+            graph.replay()
+            graph.replay()
+    torch.cuda.synchronize()
+    for r, ref in got + [(r, ref) for _, r, ref in graphs]:
+        assert torch.equal(r[0], ref[0]) and torch.equal(r[1], ref[1])
+    assert M.status_poll() == 0
+
+
+@gpu
 def test_decode_ignores_what_lies_behind():
     """Slots from seq_lens on may hold anything: NaN and infinite scales change nothing."""
     def spoil(k, v, table):
