@@ -114,14 +114,16 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   }
 }
 
-// 4-bit rows (int4.cuh): one warp per token and HPW of its KV heads, bound by its 640 bytes read
-// and 180 written per head.  Lane l holds key dims 8 l .. 8 l + 7 (l < 24) and value dims 8 l ..
-// (l < 16), so a group of 32 dims is four neighbouring lanes, its largest magnitude two
-// shuffles, and a lane's codes one word.  Per group: scale = fp16(amax / 7), code = rint(x /
+// 4-bit rows (int4.cuh): one warp per token and HPW of its KV heads, 640 bytes read and 180
+// written per head (6750 tokens of 4 heads: 14 us, 1.6 TB/s; bound by the quantising, some 15
+// instructions an element).  A lane takes 8 dims at a time, so a group of 32 dims is four
+// neighbouring lanes, its largest magnitude two shuffles, and a lane's codes one word; the words of
+// four heads lie side by side (a head at a time left a quarter of the lanes idle in its key and
+// half in its value: 21 us).  Per group: scale = fp16(amax / 7), code = rint(x /
 // scale) + 8; 7 of amax keeps zero exact and both signs alike.  The rounding is the addition of
 // 1.5 * 2^23 + 8, whose low four bits are the code.  One bf16 element in 600 lies exactly between
 // two codes, where x * (1 / scale) may end on the wrong side: the remainder x - n * scale, which
-// is exact, says so (a division per element instead: 42 us against 19 for 6750 tokens of 4 heads).
+// is exact, says so (a division per element instead took twice the time).
 // All heads of a token turn by the same angles: with many tokens a warp takes four of them and
 // computes the angles once.
 constexpr float kRound = 12582920.f;
@@ -177,46 +179,62 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams 
     }
     return w;
   };
-  uint4 kr[HPW], vr[HPW];
+  // the heads' words of 8 dims side by side, 32 at a time: word m is word m % 24 of key m / 24, or
+  // m % 16 of value m / 16
+  constexpr int kK = (24 * HPW + 31) / 32, kV = (16 * HPW + 31) / 32;
+  const uint16_t* const k_row = p.k_new + (long(t) * p.hkv + g0) * kDqk;
+  const uint16_t* const v_row = p.v_new + (long(t) * p.hkv + g0) * kDv;
+  uint4 kr[kK], vr[kV];
 #pragma unroll
-  for (int h = 0; h < HPW; ++h) {
-    const long r = long(t) * p.hkv + g0 + h;
-    kr[h] = lane < 24 ? __ldg(reinterpret_cast<const uint4*>(p.k_new + r * kDqk) + lane) : make_uint4(0, 0, 0, 0);
-    vr[h] = lane < 16 ? __ldg(reinterpret_cast<const uint4*>(p.v_new + r * kDv) + lane) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kK; ++i) {
+    const int m = 32 * i + lane;
+    kr[i] = m < 24 * HPW ? __ldg(reinterpret_cast<const uint4*>(k_row) + m) : make_uint4(0, 0, 0, 0);
   }
-  // lanes 0..3 hold dims 8 l + i, lanes 4..7 their partners + 32: x' = x c -+ y s
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int m = 32 * i + lane;
+    vr[i] = m < 16 * HPW ? __ldg(reinterpret_cast<const uint4*>(v_row) + m) : make_uint4(0, 0, 0, 0);
+  }
+  // words 0..3 of a key hold dims 8 w + i, words 4..7 their partners + 32: x' = x c -+ y s.  24 and 32
+  // are multiples of 8, so partners are four lanes apart whatever the head
   float c, sn, ci[8], si[8];
   rope_cos_sin_fine(pos, p.rope.inv_freq[lane], &c, &sn);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     ci[i] = __shfl_sync(0xffffffffu, c, 8 * (lane & 3) + i);
     si[i] = __shfl_sync(0xffffffffu, sn, 8 * (lane & 3) + i);
-    if (lane < 4) si[i] = -si[i];
+    if (!(lane & 4)) si[i] = -si[i];
+  }
+  const long block0 = entry / slots * p.hkv + g0;
+#pragma unroll
+  for (int i = 0; i < kK; ++i) {
+    const int m = 32 * i + lane, h = m / 24, w = m - 24 * h;
+    float x[8], scale;
+    widen(kr[i], x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = __shfl_xor_sync(0xffffffffu, x[e], 4);
+      if (w < 8) x[e] = x[e] * ci[e] + y * si[e];
+    }
+    const uint32_t word = quantise(x, kF16Max, scale);
+    if (m < 24 * HPW) {
+      uint8_t* const kb = reinterpret_cast<uint8_t*>(p.k_cache) + (block0 + h) * (long(slots) * kI4KSlot);
+      reinterpret_cast<uint32_t*>(kb + long(slot) * kI4KCodes)[(w & 3) * 6 + (w >> 2)] = word;
+      if ((w & 3) == 0)
+        reinterpret_cast<__half*>(kb + long(slots) * kI4KCodes)[slot * kI4KGroups + (w >> 2)] = __float2half_rn(scale);
+    }
   }
 #pragma unroll
-  for (int h = 0; h < HPW; ++h) {
-    const long block = entry / slots * p.hkv + g0 + h;
-    uint8_t* kb = reinterpret_cast<uint8_t*>(p.k_cache) + block * (long(slots) * kI4KSlot);
-    uint8_t* vb = reinterpret_cast<uint8_t*>(p.v_cache) + block * (long(slots) * kI4VSlot);
+  for (int i = 0; i < kV; ++i) {
+    const int m = 32 * i + lane, h = m / 16, w = m % 16;
     float x[8], scale;
-    widen(kr[h], x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = __shfl_xor_sync(0xffffffffu, x[i], 4);
-      if (lane < 8) x[i] = x[i] * ci[i] + y * si[i];
-    }
-    const uint32_t kw = quantise(x, kF16Max, scale);
-    if (lane < 24) {
-      reinterpret_cast<uint32_t*>(kb + long(slot) * kI4KCodes)[(lane & 3) * 6 + (lane >> 2)] = kw;
-      if ((lane & 3) == 0)
-        reinterpret_cast<__half*>(kb + long(slots) * kI4KCodes)[slot * kI4KGroups + (lane >> 2)] = __float2half_rn(scale);
-    }
-    widen(vr[h], x);
-    const uint32_t vw = quantise(x, kI4VScaleMax, scale);
-    if (lane < 16) {
-      reinterpret_cast<uint32_t*>(vb + long(slot) * kI4VCodes)[lane] = vw;
-      if ((lane & 3) == 0)
-        reinterpret_cast<__half*>(vb + long(slots) * kI4VCodes)[slot * kI4VGroups + (lane >> 2)] = __float2half_rn(scale);
+    widen(vr[i], x);
+    const uint32_t word = quantise(x, kI4VScaleMax, scale);
+    if (m < 16 * HPW) {
+      uint8_t* const vb = reinterpret_cast<uint8_t*>(p.v_cache) + (block0 + h) * (long(slots) * kI4VSlot);
+      reinterpret_cast<uint32_t*>(vb + long(slot) * kI4VCodes)[w] = word;
+      if ((w & 3) == 0)
+        reinterpret_cast<__half*>(vb + long(slots) * kI4VCodes)[slot * kI4VGroups + (w >> 2)] = __float2half_rn(scale);
     }
   }
   if (range) atomicOr(p.status, MIMO_STATUS_RANGE);
