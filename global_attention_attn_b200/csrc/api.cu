@@ -271,6 +271,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   p.tc = plan.tc;
   p.nc = plan.nc;
   p.groups = plan.groups;
+  p.split = plan.split;
   p.stages = plan.stages;
   p.workers = plan.workers;
   p.whole_units = plan.whole_units;

@@ -81,6 +81,7 @@ struct Decode4Params {
   CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, tile, 1}
   int batch, hkv, group, q_len, n_blocks;
   int tc;                      // decode_int4_tc.cu (pages), else decode_int4.cu (rings)
+  int split;                   // rings: groups that share a worker's units
   int nc, groups, stages;      // rings: warps per worker (one per row block), workers per CTA, stages per worker
   int workers;                 // at most
   int whole_units;             // pieces hold whole (sequence, KV head) units: no combine
@@ -106,7 +107,7 @@ struct Decode4Params {
 };
 struct Decode4Plan {
   int tc;
-  int tile, n_blocks, nc, groups, stages, workers, whole_units;
+  int tile, n_blocks, nc, groups, split, stages, workers, whole_units;
 };
 
 // Attention weights per cached slot (weights.cu).

@@ -387,6 +387,25 @@ def test_decode_ring(ring, q_len, window, hkv):
 
 
 @gpu
+@pytest.mark.parametrize("B", [74, 80, 160])
+def test_decode_many_rings(B):
+    """More rings than workers, as many as pairs of them, and numbers between."""
+    g, r = gen(48), np.random.default_rng(48)
+    ctx = [int(x) for x in r.integers(1, 700, B)]
+    k, v, _, _ = R.random_cache(R.INT4, B, g, 8, 128)
+    q = torch.randn((B, 64, 192), generator=g, device="cuda").bfloat16()
+    out, lse = M.mimo_attn_decode(q, R.i32(ctx), max_seq_len=700, num_kv_heads=8, rope_base=1e4, window=128, cache_kind=RING,
+                                  k_cache=k, v_cache=v, cache_dtype=M.MIMO_DTYPE_INT4)
+    assert M.status_poll() == 0
+    for s in range(0, B, 9):
+        n = ctx[s]
+        at = torch.arange(max(0, n - 128), n, device="cuda")
+        kv, vv = R.slots_of(k[s:s + 1], R.INT4, 192)[0], R.slots_of(v[s:s + 1], R.INT4, 128)[0]
+        R.Row(q[s:s + 1], kv[:, at % 128], vv[:, at % 128], at, torch.arange(n - 1, n, device="cuda"), 1e4,
+              window=128).check(out[s:s + 1], lse[s:s + 1], f"ring {s}")
+
+
+@gpu
 def test_decode_noalloc_and_streams():
     """The no-alloc call on a big batch (its pieces are cut to the array), a second stream, and
     a captured call replayed on new contents."""
