@@ -52,8 +52,7 @@ __device__ __forceinline__ uint2 warps_before(uint32_t* buf, uint32_t mine, int 
 
 // One cluster per (sequence, KV head) row.  The row is read once (4 bytes a slot, the floor) by the
 // cluster's 1..8 CTAs, and stays with them: 4 Q keys a thread in registers, or in shared memory
-// for the longest rows.  A lane takes 4 neighbouring slots at a step, a warp 128, so that order
-// costs one scan per 128 slots.  The border is found by up to three histogram passes (a CTA adds
+// for the longest rows.  A lane takes 4 neighbouring slots at a step, a warp 128.  The border is found by up to three histogram passes (a CTA adds
 // its bins that hold anything to those of one of the cluster through distributed shared memory,
 // and every CTA draws the same conclusion from these: 56 us for 16 sequences of 40000..131072
 // slots and 4 heads, against 65 with every CTA reading the bins of all; a pass whose bin is wanted
@@ -213,6 +212,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   });
   more = __reduce_add_sync(0xffffffffu, more);
   tie = __reduce_add_sync(0xffffffffu, tie);
+  const bool ties = tie > 0 && take > 0;  // this warp may have to choose
   __syncthreads();  // (the last pass's sums are read)
   const uint2 m = warps_before(sums[0], more, warp, lane), t = warps_before(sums[1], tie, warp, lane);
   more = m.x;
@@ -232,35 +232,35 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   int32_t* const idx = p.idx + long(row) * p.keep;
   float* const out = p.scores_out ? p.scores_out + long(row) * p.keep : nullptr;
   each([&](int k, const uint32_t* key) {
-    // both counts of the lane's four, scanned over the warp in one word (each at most 128)
-    uint32_t mine = 0;
+    // places by votes: slots of lower lanes, then the lane's own
+    uint32_t up[4], eq[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) mine += ((key[e] & mask) > prefix ? 1u : 0u) + ((key[e] & mask) == prefix ? 0x10000u : 0u);
-    if (!__any_sync(0xffffffffu, mine)) return;
-    uint32_t incl = mine;
+    for (int e = 0; e < 4; ++e) up[e] = __ballot_sync(0xffffffffu, (key[e] & mask) > prefix);
+    if (ties)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += u;
+      for (int e = 0; e < 4; ++e) eq[e] = __ballot_sync(0xffffffffu, (key[e] & mask) == prefix);
+    if (!(up[0] | up[1] | up[2] | up[3] | eq[0] | eq[1] | eq[2] | eq[3])) return;
+    const uint32_t lower = (1u << lane) - 1;
+    uint32_t mo = more, ti = tie;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      mo += __popc(up[e] & lower);
+      ti += __popc(eq[e] & lower);
+      more += __popc(up[e]);
+      tie += __popc(eq[e]);
     }
-    uint32_t mo = more + ((incl - mine) & 0xFFFFu), ti = tie + ((incl - mine) >> 16);
-    if (mine) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool up = (key[e] & mask) > prefix, eq = (key[e] & mask) == prefix;
-        if (up || (eq && ti < take)) {
-          const uint32_t j = mo + min(ti, take);
-          const int slot = at0 + 128 * k + e;
-          idx[j] = slot;
-          if (out) out[j] = exact_key(key[e]) ? key_score(key[e]) : __ldg(src + slot);
-        }
-        mo += up;
-        ti += eq;
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t u = (up[e] >> lane) & 1, q = (eq[e] >> lane) & 1;
+      if (u || (q && ti < take)) {
+        const uint32_t j = mo + min(ti, take);
+        const int slot = at0 + 128 * k + e;
+        idx[j] = slot;
+        if (out) out[j] = exact_key(key[e]) ? key_score(key[e]) : __ldg(src + slot);
       }
+      mo += u;
+      ti += q;
     }
-    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
-    more += total & 0xFFFFu;
-    tie += total >> 16;
   });
   const int count = min(L, p.keep);
   for (int j = count + rank * kSelThreads + tid; j < p.keep; j += C * kSelThreads) {
