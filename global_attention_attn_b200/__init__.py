@@ -371,6 +371,11 @@ def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_head
     return scores
 
 
+def _check32(t, size: int, name: str):
+    if t.numel() != size or t.element_size() != 4 or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous 32-bit tensor of {size} elements")
+
+
 def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int = 0, first: int = 0, idx=None,
                    counts=None, scores_out=None, stream=None):
     """The slots that stay of every (sequence, KV head): the first `first`, the last `recent`, and the
@@ -381,15 +386,18 @@ def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int
     if scores.ndim != 3 or not scores.is_contiguous() or scores.element_size() != 4:
         raise ValueError("scores is a contiguous float32 [num_seqs, num_kv_heads, slots] tensor")
     n, h, slots = scores.shape
-    for t, size, name in ((idx, n * h * keep, "idx"), (counts, n, "counts"), (scores_out, n * h * keep, "scores_out")):
-        if t is not None and (t.numel() != size or t.element_size() != 4 or not t.is_contiguous()):
-            raise ValueError(f"{name} is a contiguous 32-bit tensor of {size} elements")
     if idx is None:
         idx = scores.new_empty((n, h, keep), dtype=torch.int32)
+    else:
+        _check32(idx, n * h * keep, "idx")
     if counts is None:
         counts = scores.new_empty((n,), dtype=torch.int32)
+    else:
+        _check32(counts, n, "counts")
     if scores_out is None:
         scores_out = scores.new_empty((n, h, keep), dtype=torch.float32)
+    else:
+        _check32(scores_out, n * h * keep, "scores_out")
     a = MimoSelectArgs()
     a.num_seqs, a.num_kv_heads, a.scores, a.score_stride = n, h, _ptr(scores), slots
     a.seq_lens, a.max_seq_len = _ptr(seq_lens), int(max_seq_len)

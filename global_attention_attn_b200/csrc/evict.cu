@@ -278,8 +278,10 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
   const int steps = (per + 128 * kSelWarps - 1) / (128 * kSelWarps);
   auto kernel = steps <= 2 ? select_kernel<2> : (steps <= 8 ? select_kernel<8> : select_kernel<0>);
   const size_t bytes = steps <= 8 ? 0 : size_t(steps) * 128 * kSelWarps * 4;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-  if (e != cudaSuccess) return e;
+  if (bytes > 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.num_seqs) * p.hkv * c);
   cfg.blockDim = dim3(kSelThreads);
