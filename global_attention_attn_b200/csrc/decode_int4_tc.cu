@@ -21,7 +21,7 @@
 // Eight warps (two threads a key) work on a tile, another issues copies and products.  One token
 // of a KV head is 16 columns, whose tensor and shared memory let two such streams share an SM; more
 // columns have one stream.  (Four threads a key: 4 and 8 drafts 103 and 215 us against 97 and 195
-// below, the work that does not divide by columns done twice.)  From 64 columns on the six group
+// at the time, the work that does not divide by columns done twice.)  From 64 columns on the six group
 // sums do not fit beside the output's, so the logits run in two or three parts that take turns in
 // the same columns; an SM's warps hide the wait between them with the next tile's keys.
 // Workers are the streams: the tiles of all sequences and KV heads form one line, cut into as many
@@ -30,13 +30,13 @@
 // their rows directly; contexts of up to 256 keys are cut between units only.
 //
 // Measured (graph replay, in brackets the same on mma.sync with the drafts' rows in warps of their
-// own): 64 sequences of 4096..65536 keys, one token, 430 us (548), 3.6 TB/s, 0.55 of a copy's rate;
-// one of 131001 keys 41 us (64); one of 500 12.4 us (18.5); 16 of 1001..16384 with 1, 2, 4, 8
-// drafts 45, 64, 97 (160), 195 us.  Bound by the warps' instructions, 540 per warp and tile of
-// 16 columns (half of them the unpacking): without its copies' arithmetic the first call takes
-// 260 us.  Short calls are the sum of what a worker does once: 2 us to its first tile's copy,
-// 1.5 us for the query operand, 3 us for the first tile (nothing overlaps yet, the references are
-// set) and 1.5 us for its rows.
+// own): 64 sequences of 4096..65536 keys, one token, 412 us (548), 3.7 TB/s, 0.57 of a copy's rate;
+// one of 131001 keys 39 us (64); one of 500 12.4 us (18.5); 16 of 1001..16384 with 1, 2, 4, 8
+// drafts 43, 62, 92 (160), 186 us.  Bound by the warps' instructions, 540 per warp and tile of
+// 16 columns (a third of them the unpacking): the copies alone take 260 us in the first call.
+// Short calls are the sum of what a worker does once: 2 us to its first tile's copy, 1.5 us for the
+// query operand, 3 us for the first tile (nothing overlaps yet, the references are set) and 1.5 us
+// for its rows.
 #include "int4_tc.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
