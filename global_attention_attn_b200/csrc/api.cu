@@ -972,7 +972,7 @@ int mimo_kv_select(const mimo_select_args* a, void* stream) {
   p.counts = a->counts;
   p.scores_out = a->scores_out;
   p.status = d.status;
-  cudaError_t e = launch_select(p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_select(p, d.sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MIMO_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return MIMO_OK;
 }

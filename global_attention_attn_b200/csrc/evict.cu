@@ -30,22 +30,22 @@ __device__ __forceinline__ float key_score(uint32_t k) { return __uint_as_float(
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;  // 11, 11 and 10 bits a pass
-static_assert(kBins == 4 * kSelThreads, "a thread's bins are one 16-byte read");
+constexpr int kBinThreads = kBins / 4;  // a thread's bins are one 16-byte read
 
 // Sum over the warps before this one, and over all, of one value per warp (a block-wide call).
+template <int W>  // warps
 __device__ __forceinline__ uint2 warps_before(uint32_t* buf, uint32_t mine, int warp, int lane) {
   if (lane == 0) buf[warp] = mine;
   __syncthreads();
-  const uint32_t v = lane < kSelWarps ? buf[lane] : 0u;
+  const uint32_t v = lane < W ? buf[lane] : 0u;
   uint32_t incl = v;
 #pragma unroll
-  for (int d = 1; d < kSelWarps; d <<= 1) {
+  for (int d = 1; d < W; d <<= 1) {
     const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += u;
   }
-  return make_uint2(__shfl_sync(0xffffffffu, incl - v, warp), __shfl_sync(0xffffffffu, incl, kSelWarps - 1));
+  return make_uint2(__shfl_sync(0xffffffffu, incl - v, warp), __shfl_sync(0xffffffffu, incl, W - 1));
 }
 
 }  // namespace
@@ -60,11 +60,12 @@ __device__ __forceinline__ uint2 warps_before(uint32_t* buf, uint32_t mine, int 
 // the kept slots at the place that the counts of the parts before it give: ascending, equal
 // scores lowest slot first.  Slots never attended all score 0, so zeros are counted aside and
 // enter the histogram once per warp; other equal scores add up one by one.
-template <int Q>  // steps a warp holds in registers; 0: in shared memory
-__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ uint4 row_keys[];  // Q == 0: this CTA's part of the row
+template <int T, int Q>  // threads; steps a warp holds in registers
+__global__ void __launch_bounds__(T, 1024 / T) select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kWarps = T / 32;
+  extern __shared__ uint4 rest_keys[];  // the steps after them, [step][thread]
   __shared__ __align__(16) uint32_t hist[3][kBins];
-  __shared__ uint32_t sums[2][kSelWarps];
+  __shared__ uint32_t sums[2][kWarps];
   __shared__ uint32_t found[3][3];  // of a pass: the border's bin, how many of it are wanted, how many it holds
   __shared__ uint32_t part[2];      // this CTA's counts, for the CTAs behind it
   cg::cluster_group cl = cg::this_cluster();
@@ -76,14 +77,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     L = max(0, min(L, p.max_seq_len));
   }
 #pragma unroll
-  for (int i = 0; i < 3; ++i) reinterpret_cast<uint4*>(hist[i])[tid] = make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 3; ++i)
+    if (tid < kBinThreads) reinterpret_cast<uint4*>(hist[i])[tid] = make_uint4(0, 0, 0, 0);
   if (C > 1) cluster_arrive();
   const float* const src = p.scores + long(row) * p.score_stride;
   const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
   const int per = ((L + C - 1) / C + 127) & ~127;  // slots of a CTA
   const int lo = min(L, rank * per), end = min(L, lo + per);
   // a warp's contiguous range of slots, 128 at a step
-  const int range = (((end - lo) + kSelWarps - 1) / kSelWarps + 127) & ~127, steps = range / 128;
+  const int range = (((end - lo) + kWarps - 1) / kWarps + 127) & ~127, steps = range / 128;
   const int at0 = lo + warp * range + 4 * lane, at_end = min(end, lo + (warp + 1) * range);
   // Keys: of a slot that stays whatever its score (the first, the recent; every slot of a row that
   // fits) the largest there is, above any score's; where there is no slot 0, below any score's.
@@ -118,29 +120,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     for (int e = 0; e < 4; ++e) zeros += key[e] == kZeroKey;
     return make_uint4(key[0], key[1], key[2], key[3]);
   };
-  uint4 reg[Q ? Q : 1];
-  if constexpr (Q > 0) {
+  uint4 reg[Q];
 #pragma unroll
-    for (int k = 0; k < Q; ++k) reg[k] = k < steps ? load(k) : make_uint4(0, 0, 0, 0);
-  } else {
-    for (int k = 0; k < steps; ++k) row_keys[(warp * range >> 2) + 32 * k + lane] = load(k);
-  }
+  for (int k = 0; k < Q; ++k) reg[k] = k < steps ? load(k) : make_uint4(0, 0, 0, 0);
+  for (int k = Q; k < steps; ++k) rest_keys[(k - Q) * T + tid] = load(k);
   zeros = __reduce_add_sync(0xffffffffu, zeros);
   // f(step, 4 keys) for every 128 slots of this warp, in order
   auto each = [&](auto&& f) {
-    if constexpr (Q > 0) {
 #pragma unroll
-      for (int k = 0; k < Q; ++k)
-        if (k < steps) {
-          const uint32_t key[4] = {reg[k].x, reg[k].y, reg[k].z, reg[k].w};
-          f(k, key);
-        }
-    } else {
-      for (int k = 0; k < steps; ++k) {
-        const uint4 v = row_keys[(warp * range >> 2) + 32 * k + lane];
-        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+    for (int k = 0; k < Q; ++k)
+      if (k < steps) {
+        const uint32_t key[4] = {reg[k].x, reg[k].y, reg[k].z, reg[k].w};
         f(k, key);
       }
+#pragma unroll 1
+    for (int k = Q; k < steps; ++k) {
+      const uint4 v = rest_keys[(k - Q) * T + tid];
+      const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+      f(k, key);
     }
   };
   int need = p.keep;
@@ -162,7 +159,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     const int leader = pass % C;
     __syncthreads();
     if (C > 1) {
-      if (rank != leader) {
+      if (rank != leader && tid < kBinThreads) {
         uint32_t* const to = cl.map_shared_rank(hs, leader);
         const uint4 v = reinterpret_cast<const uint4*>(hs)[tid];
         const uint32_t mine[4] = {v.x, v.y, v.z, v.w};
@@ -173,7 +170,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
       cl.sync();
     }
     // bins from the largest down, 4 a thread
-    const uint4 b4 = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hs, leader) + kBins - 4 - 4 * tid);
+    uint4 b4 = make_uint4(0, 0, 0, 0);
+    if (tid < kBinThreads) b4 = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hs, leader) + kBins - 4 - 4 * tid);
     const uint32_t h[4] = {b4.w, b4.z, b4.y, b4.x};
     const uint32_t sum = h[0] + h[1] + h[2] + h[3];
     uint32_t incl = sum;
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
       const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += u;
     }
-    uint32_t before = incl - sum + warps_before(sums[pass & 1], __shfl_sync(0xffffffffu, incl, 31), warp, lane).x;
+    uint32_t before = incl - sum + warps_before<kWarps>(sums[pass & 1], __shfl_sync(0xffffffffu, incl, 31), warp, lane).x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (before < uint32_t(need) && before + h[e] >= uint32_t(need)) {
@@ -214,7 +212,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   tie = __reduce_add_sync(0xffffffffu, tie);
   const bool ties = tie > 0 && take > 0;  // this warp may have to choose
   __syncthreads();  // (the last pass's sums are read)
-  const uint2 m = warps_before(sums[0], more, warp, lane), t = warps_before(sums[1], tie, warp, lane);
+  const uint2 m = warps_before<kWarps>(sums[0], more, warp, lane), t = warps_before<kWarps>(sums[1], tie, warp, lane);
   more = m.x;
   tie = t.x;
   if (C > 1) {
@@ -263,7 +261,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     }
   });
   const int count = min(L, p.keep);
-  for (int j = count + rank * kSelThreads + tid; j < p.keep; j += C * kSelThreads) {
+  for (int j = count + rank * T + tid; j < p.keep; j += C * T) {
     idx[j] = -1;
     if (out) out[j] = 0.f;
   }
@@ -271,20 +269,26 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   if (C > 1) cl.sync();  // no CTA leaves while another reads its bins or counts
 }
 
-cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
-  int c = 1;  // CTAs per row: 4096 slots each at least, 8 at most
+cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t s) {
+  const long rows = long(p.num_seqs) * p.hkv;
+  int c = 1, threads = 512;  // CTAs per row: 4096 slots each at least, 8 at most
   while (c < 8 && c * 4096 < p.max_seq_len) c *= 2;
+  if (c > 1 && rows * c > 2 * sms) {
+    // more than a round of them: fewer CTAs of twice the threads and at most 65536 slots
+    threads = 1024;
+    for (c = 1; c < 8 && c * 65536 < p.max_seq_len;) c *= 2;
+  }
   const int per = ((p.max_seq_len + c - 1) / c + 127) & ~127;
-  const int steps = (per + 128 * kSelWarps - 1) / (128 * kSelWarps);
-  auto kernel = steps <= 2 ? select_kernel<2> : (steps <= 8 ? select_kernel<8> : select_kernel<0>);
-  const size_t bytes = steps <= 8 ? 0 : size_t(steps) * 128 * kSelWarps * 4;
+  const int steps = (per + 4 * threads - 1) / (4 * threads);
+  auto kernel = threads == 1024 ? select_kernel<1024, 8> : (steps <= 2 ? select_kernel<512, 2> : select_kernel<512, 8>);
+  const size_t bytes = steps <= 8 ? 0 : size_t(steps - 8) * 16 * threads;
   if (bytes > 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.num_seqs) * p.hkv * c);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.gridDim = dim3(unsigned(rows * c));
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cudaLaunchAttribute at[1];

@@ -249,7 +249,7 @@ cudaError_t launch_decode4_combine(const Decode4Params& p, cudaStream_t s);
 cudaError_t launch_decode4(const Decode4Params& p, int sms, cudaStream_t s, void* ev_begin, void* ev_end);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t s);
 cudaError_t launch_weights_int4(WeightsParams p, int sms, cudaStream_t s);
-cudaError_t launch_select(const SelectParams& p, cudaStream_t s);
+cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t s);
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t s);
 cudaError_t launch_rope_k(const RopeKParams& p, cudaStream_t s);
 // kind 0: sliding window (G=8 heads x 16 rows, one 144-key tile); kind 1: global (G=16 x 8 rows, 128-key tiles)
