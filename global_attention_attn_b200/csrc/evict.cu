@@ -51,11 +51,11 @@ __device__ __forceinline__ uint2 warps_before(uint32_t* buf, uint32_t mine, int 
 }  // namespace
 
 // One cluster per (sequence, KV head) row.  The row is read once (4 bytes a slot, the floor) by the
-// cluster's 1..8 CTAs, and stays with them: 4 Q keys a thread in registers, or in shared memory
-// for the longest rows.  A lane takes 4 neighbouring slots at a step, a warp 128.  The border is found by up to three histogram passes (a CTA adds
+// cluster's 1..8 CTAs, and stays with them: 4 Q keys a thread in registers, the rest of the longest
+// rows in shared memory.  A lane takes 4 neighbouring slots at a step, a warp 128.  The border is found by up to three histogram passes (a CTA adds
 // its bins that hold anything to those of one of the cluster through distributed shared memory,
-// and every CTA draws the same conclusion from these: 56 us for 16 sequences of 40000..131072
-// slots and 4 heads, against 65 with every CTA reading the bins of all; a pass whose bin is wanted
+// and every CTA draws the same conclusion from these: at 16 sequences of 40000..131072
+// slots and 4 heads a seventh faster than every CTA reading the bins of all; a pass whose bin is wanted
 // whole is the last), then each CTA writes its part of
 // the kept slots at the place that the counts of the parts before it give: ascending, equal
 // scores lowest slot first.  Slots never attended all score 0, so zeros are counted aside and
@@ -273,8 +273,13 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t s) {
   const long rows = long(p.num_seqs) * p.hkv;
   int c = 1, threads = 512;  // CTAs per row: 4096 slots each at least, 8 at most
   while (c < 8 && c * 4096 < p.max_seq_len) c *= 2;
-  if (c > 1 && rows * c > 2 * sms) {
-    // more than a round of them: fewer CTAs of twice the threads and at most 65536 slots
+  // Where an SM cannot hold two of them, or all the rows' CTAs are more than one round, fewer CTAs of
+  // twice the threads and at most 65536 slots: fewer barriers across CTAs, and no second round
+  // (us, with / without: 16 sequences of 40000..131072 slots and 4 heads 47 / 56, 32 of 20000..32768
+  // 27 / 65, 64 of 4000..16384 29 / 46, 8 of 300000..390000 113 / 123; but one of 30000, a single
+  // round, 18.6 / 16.4, and 4 of 100000..131072 45 / 30).
+  const int resident = (p.max_seq_len + c - 1) / c > 19 * 2048 ? 1 : 2;
+  if (c > 1 && rows * c > resident * sms) {
     threads = 1024;
     for (c = 1; c < 8 && c * 65536 < p.max_seq_len;) c *= 2;
   }

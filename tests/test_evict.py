@@ -261,6 +261,20 @@ def test_select(lens, keep, recent, first, hkv):
 
 
 @gpu
+@pytest.mark.parametrize("B, lo, hi, keep, recent", [(40, 5000, 9000, 2000, 64), (16, 70000, 140000, 9000, 0), (20, 1, 66000, 3000, 9),
+                                                     (5, 300000, 390000, 20000, 128)])
+def test_select_many_rows(B, lo, hi, keep, recent):
+    """More rows than one round of CTAs holds; half of the scores are equal."""
+    g = gen(B)
+    lens = [int(x) for x in np.random.default_rng(B).integers(lo, hi + 1, B)]
+    scores = torch.randn((B, 8, max(lens)), generator=g, device="cuda")
+    scores = torch.where(torch.rand(scores.shape, generator=g, device="cuda") < 0.5, torch.full_like(scores, 0.5), scores)
+    check_select(scores, lens, keep, recent, 4)
+    scores[scores == 0.5] = 0.0
+    check_select(scores, lens, lo // 2 + 5 + recent, recent, 4)
+
+
+@gpu
 @pytest.mark.parametrize("n", [500, 9000, 50001])
 def test_select_ties_and_specials(n):
     g = gen(n)
