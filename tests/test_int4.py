@@ -442,6 +442,30 @@ def test_decode_noalloc_and_streams():
 
 
 @gpu
+@pytest.mark.parametrize("kind", [PAGED, RING])
+def test_decode_kernel_events(kind):
+    """The events around the decode kernel, the merge behind them."""
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for e in ev:
+        e.record()
+    g = gen(49)
+    q = torch.randn((1, 64, 192), generator=g, device="cuda").bfloat16()
+    if kind == PAGED:
+        table, pages = R.table_of([5000], np.random.default_rng(49))
+        k, v, _, _ = R.random_cache(R.INT4, pages, g)
+        kw = dict(num_kv_heads=4, window=0, block_table=table, num_pages=pages)
+    else:
+        k, v, _, _ = R.random_cache(R.INT4, 1, g, 8, 128)
+        kw = dict(num_kv_heads=8, window=128)
+    run = lambda **e: M.mimo_attn_decode(q, R.i32([5000]), max_seq_len=5000, rope_base=1e6, cache_kind=kind, k_cache=k,
+                                         v_cache=v, cache_dtype=M.MIMO_DTYPE_INT4, **kw, **e)
+    a, b = run(), run(kernel_events=ev)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert 0 < ev[0].elapsed_time(ev[1]) < 50
+
+
+@gpu
 def test_decode_repeats_bit_for_bit():
     a = check_paged([9000, 20, 700], seed=53)
     b = check_paged([9000, 20, 700], seed=53)
