@@ -227,13 +227,11 @@ size_t decode_workspace(int batch, int q_len, int max_seq_len, int window) {
 
 // Segments of a 4-bit decode's workers, and the tile table its combine reads.
 size_t decode4_workspace(const Decode4Plan& d, int batch) {
-  if (d.whole_units) return 0;
+  if (d.no_pieces) return 0;
   const size_t rows = 2 * size_t(d.workers) * d.n_blocks * 16;
   return round256(rows * kDv * 4) + round256(rows * 2 * 4) +
          round256((size_t(batch < kMaxTableBatch ? batch : kMaxTableBatch) + 1) * 8);
 }
-// The plan never counts on more SMs than this, so that the size query needs no device.
-constexpr int kI4Sms = 148;
 
 // mimo_attn_decode on a 4-bit cache, after its checks.
 int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_slots, size_t room, void* stream) {
@@ -248,7 +246,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   Decode4Plan plan = decode4_plan(a->batch < kMaxTableBatch ? a->batch : kMaxTableBatch, hkv, q_len,
                                   ring ? ring_slots : decode_unit_keys(a->max_seq_len, a->layer.window, q_len), ring,
                                   d.sms < kI4Sms ? d.sms : kI4Sms);
-  while (plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
+  while (!plan.whole_units && plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
   const long tiles = a->max_seq_len / kPage + 2L;
   if (!ring && (long(a->num_pages) * hkv > INT_MAX || tiles * (a->batch < kMaxTableBatch ? a->batch : kMaxTableBatch) * hkv > INT_MAX))
     return fail(MIMO_ERR_UNSUPPORTED, "%s: num_pages * num_kv_heads, or the pages of max_seq_len in all, pass 2^31", fn);

@@ -549,9 +549,14 @@ Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring
   d.split = ring && d.nc == 1 && (long long)batch * hkv * 2 <= (long long)sms * d.groups ? 2 : 1;
   d.stages = kAllStages / d.groups;
   const int tiles = (unit_keys + d.tile - 1) / d.tile + 1;  // a window may begin inside a tile
-  // A unit of up to 256 keys stays whole: a second kernel would cost more than it saves.
-  d.whole_units = ring || unit_keys <= 256;
-  const long long units = (long long)batch * hkv, most = d.whole_units ? units : units * tiles;
+  // A unit of up to 512 keys stays whole, one of up to 1024 where there are units for a third of the
+  // workers: a second kernel would cost more than it saves (us, whole / cut, one token: 1 sequence of
+  // 500 keys 13 / 12.4, but 14 / 16.4 from Python, a launch less; 48 of 100..500 17 / 22, of 100..1000
+  // 23 / 27; 4 of 1000 19 / 14; 16 of 2000 30 / 25, 64 of 100..4000 62 / 58).
+  const long long units = (long long)batch * hkv;
+  d.no_pieces = ring || unit_keys <= 256;
+  d.whole_units = ring || unit_keys <= 512 || (unit_keys <= 1024 && units * 3 >= (long long)kI4Sms * d.groups);
+  const long long most = d.whole_units ? units : units * tiles;
   const long long all = (long long)sms * d.groups / d.split;
   d.workers = int(most < all ? most : all);
   return d;

@@ -27,7 +27,7 @@
 // Workers are the streams: the tiles of all sequences and KV heads form one line, cut into as many
 // equal pieces as there are workers, so any mix of lengths loads every SM alike.  A piece's first
 // and last (sequence, head) may be partial and go through the combine kernel, the others write
-// their rows directly; contexts of up to 256 keys are cut between units only.
+// their rows directly; short contexts are cut between units only.
 //
 // Measured (graph replay, in brackets the same on mma.sync with the drafts' rows in warps of their
 // own): 64 sequences of 4096..65536 keys, one token, 412 us (548), 3.7 TB/s, 0.57 of a copy's rate;
@@ -146,6 +146,9 @@ __device__ __forceinline__ void logits_part(uint32_t tmem, uint64_t qd, uint64_t
   logit_steps<N, PT, 2 * Lay<N>::kPer * PT>(tmem, uint32_t(qd), uint32_t(qd >> 32));
 }
 
+// Pieces that a line of `total` tiles is cut into: piece w is tiles w total / W .. (w + 1) total / W.
+__device__ __forceinline__ int pieces_of(long long total, int workers) { return int(total < workers ? total : workers); }
+
 // Keys a sequence's unit covers: [lo, hi], and its first tile and tile count.
 struct Span {
   int lo, hi, t0, nt;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
     }
   } else if (total > 0) {
     // (total fits 31 bits, W * W too: w total / W without a 64-bit division)
-    const int W = pieces_of(total, 1, p.workers);
+    const int W = pieces_of(total, p.workers);
     const unsigned each = unsigned(total) / W, rest = unsigned(total) - each * W;
     if (w < W) {
       a = (long long)w * each + w * rest / W;
@@ -778,7 +781,7 @@ __global__ void __launch_bounds__(kRow == 1 ? 128 : 32 * kRow) decode4_combine_k
   const long long nt = p.ws_tbl[s + 1] - p.ws_tbl[s];
   if (nt == 0) return;
   const long long u0 = p.ws_tbl[s] * p.hkv + g * nt;
-  const int W = pieces_of(total, 1, p.workers);
+  const int W = pieces_of(total, p.workers);
   const int w0 = int(((u0 + 1) * W - 1) / total), w1 = int(((u0 + nt) * W - 1) / total);
   if (w0 == w1) return;  // one piece holds the unit: its rows are written
   const int rows = p.n_blocks * 16, rr = (qrow - s * p.q_len) * p.group + h % p.group;

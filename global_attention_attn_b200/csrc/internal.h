@@ -76,6 +76,7 @@ struct DecodeParams {
 // Decode over a 4-bit cache (decode_int4.cu).
 constexpr int kI4Tile = 32;        // keys per tile of a ring
 constexpr int kI4TcTile = 128;     // and of pages
+constexpr int kI4Sms = 148;        // a plan never counts on more SMs, so that the size query needs no device
 constexpr int kMaxTableBatch = 1024;  // sequences per launch (a prefix table in shared memory)
 struct Decode4Params {
   CUtensorMap tm_v;  // value codes [blocks, slots, 64 bytes], box {64, tile, 1}
@@ -108,6 +109,7 @@ struct Decode4Params {
 struct Decode4Plan {
   int tc;
   int tile, n_blocks, nc, groups, split, stages, workers, whole_units;
+  int no_pieces;  // units so short that no batch of them is cut: no workspace
 };
 
 // Attention weights per cached slot (weights.cu).

@@ -32,12 +32,6 @@ __device__ __forceinline__ void tile_table(long long* tbl, int batch, int lane, 
   __syncwarp();
 }
 
-// Pieces that a line of `total` tiles is cut into: piece w is tiles w total / W .. (w + 1) total / W.
-__device__ __forceinline__ int pieces_of(long long total, int min_tiles, int workers) {
-  const long long w = (total + min_tiles - 1) / min_tiles;
-  return int(w < workers ? w : workers);
-}
-
 // A position on the line: sequence s's heads hold hkv * (tbl[s + 1] - tbl[s]) tiles.
 struct TileCursor {
   int s, g, t, nt;
