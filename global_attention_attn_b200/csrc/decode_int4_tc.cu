@@ -52,9 +52,14 @@ constexpr int kKBytes = kTile * kI4KSlot, kOffKs = kTile * kI4KCodes;
 constexpr int kVBytes = kTile * kI4VSlot, kOffVs = kTile * kI4VCodes;
 static_assert(kVBytes % 512 == 0, "64-byte swizzle alignment");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Weights are 2^(z - ref): ref is a column's maximum when it was set, and moves only when a logit
-// passes it by more than this many powers of two.
-constexpr float kSlack = 6.f;
+// Weights are 2^(z - ref + kPBias): ref is a column's maximum when it was set, and moves only when a
+// logit passes it by more than kSlack powers of two.  The products take them in fp16, whose smallest
+// steps are 2^-24: the bias uses all of the range above (2^(kSlack + kPBias) < 65504), so that a weight
+// keeps its digits down to 2^-24 of the reference and is not lost before 2^-35 (without it 2^-14 and
+// 2^-25: a key that takes nearly all the weight, over 131000 others at 2^-25.2 each, took their 0.4 %
+// of the sum, and with a small value of its own most of the output).  The sums of weights carry the
+// same factor; -ref + kPBias is what stands for the reference everywhere.
+constexpr float kSlack = 6.f, kPBias = 9.9375f;
 constexpr int kW = 8, kN = 32 * kW;  // warps and threads of a stream, two threads a key
 
 // What depends on the number of columns.
@@ -99,6 +104,13 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// two weights -> fp16x2 (saturating: beyond |z| = 2^19 the fp32 step of a logit is above what is left
+// between 2^(kSlack + kPBias) and fp16's limit)
+__device__ __forceinline__ uint32_t f16x2_sat_of(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 __device__ __forceinline__ float warp_max(float v) {
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
   const uint32_t base = sbase + str * Y::kStream;
   const uint32_t vt = base + Y::kOffV, pt = base + Y::kOffP;
   const uint32_t ring_k = base + Y::kOffRingK, ring_v = base + Y::kOffRingV;
-  float* const nref = reinterpret_cast<float*>(smem + Y::kOffX + str * Y::kXBytes);  // [N] minus the references
+  float* const nref = reinterpret_cast<float*>(smem + Y::kOffX + str * Y::kXBytes);  // [N] kPBias minus the references
   float* const fac = nref + N;                                                       // [N] what a move multiplies with
   float* const wmax = fac + N;                                                       // [4][N]
   float2* const cs = reinterpret_cast<float2*>(wmax + 4 * N);
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         top = fmaxf(top, t8);
       }
       // (the warps tell each other which tile moves the references; the answer is read after the values)
-      const bool raise = __any_sync(0xffffffffu, top > kSlack) || !good;
+      const bool raise = __any_sync(0xffffffffu, top > kSlack + kPBias) || !good;
       if (lane == 0) {
         if (raise) flag[x & 1] = x + 1;
         mbar_arrive(vote);
@@ -623,10 +635,10 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         }
         if (tid < N) {
           const float m = fmaxf(fmaxf(wmax[tid], wmax[N + tid]), fmaxf(wmax[2 * N + tid], wmax[3 * N + tid]));
-          const float ref = -nref[tid];
-          const bool up = m > ref + kSlack;
-          fac[tid] = up ? ex2(ref - m) : 1.f;  // (from -inf: 0, of sums that are 0)
-          if (up) nref[tid] = -m;
+          const float old = nref[tid], now = kPBias - m;
+          const bool up = m + old > kSlack + kPBias;
+          fac[tid] = up ? ex2(now - old) : 1.f;  // (from a reference of -inf: 0, of sums that are 0)
+          if (up) nref[tid] = now;
         }
         stream_sync();
 #pragma unroll
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pk[e] = f16x2_of(xs[2 * e], xs[2 * e + 1]);
+          pk[e] = f16x2_sat_of(xs[2 * e], xs[2 * e + 1]);
           l[4 * i + e] = add_f32x2(l[4 * i + e], pack_f32x2(xs[2 * e], xs[2 * e + 1]));
         }
         const int c8 = hw * (NC / 8) + i;  // of 8 columns

@@ -515,3 +515,31 @@ def test_append_then_decode():
             R.Row(q[s:s + 1], R.pages_of(kv, table[s], m), R.pages_of(vv, table[s], m), torch.arange(m, device="cuda"),
                   torch.tensor([m - 1], device="cuda"), 1e7).check(out[s:s + 1], lse[s:s + 1], f"step {i}")
     assert M.status_poll() == 0
+
+
+@gpu
+@pytest.mark.parametrize("q_len", [1, 2, 4, 8])
+def test_decode_one_dominant_key_over_a_flat_tail(q_len):
+    """A first key that takes nearly all the weight and has a zero value (what trained heads do), over
+    131000 keys whose weights are 2^20 to 2^25.5 below it, by head, and whose values share a sign: the
+    output is the tail's alone.  (In fp16 without a bias, weights below 2^-25 are zero.)"""
+    g, n = gen(70), 131001
+    table, pages = R.table_of([n], np.random.default_rng(70))
+    kc = torch.full((pages, 4, 128, 192), 8, dtype=torch.uint8, device="cuda")  # zeros: every tail logit is 0
+    vc = torch.randint(9, 16, (pages, 4, 128, 128), generator=g, device="cuda", dtype=torch.uint8)
+    first = int(table[0, 0])
+    kc[first, :, 0, 100] = 15
+    vc[first, :, 0] = 8
+    k = R.int4_block(kc, torch.ones((pages, 4, 128, 6), device="cuda"))
+    v = R.int4_block(vc, torch.rand((pages, 4, 128, 4), generator=g, device="cuda") * 0.3 + 0.05)
+    del kc, vc
+    q = torch.zeros((q_len, 64, 192), device="cuda", dtype=torch.bfloat16)
+    for i in range(q_len):  # the logit of key 0 in powers of two: 20 .. 25.5, spread differently in every draft
+        x = 20 + 5.5 * ((torch.arange(64, device="cuda") * 7 + i) % 64) / 63
+        q[i, :, 100] = (x * np.log(2.0) / (7 * R.SCALE)).bfloat16()
+    out, lse = M.mimo_attn_decode(q, R.i32([n]), max_seq_len=n, num_kv_heads=4, rope_base=1e7, window=0, cache_kind=PAGED,
+                                  k_cache=k, v_cache=v, block_table=table, num_pages=pages, cache_dtype=M.MIMO_DTYPE_INT4,
+                                  q_len=q_len)
+    assert M.status_poll() == 0
+    kv, vv = (R.pages_of(R.slots_of(c, R.INT4, d), table[0], n) for c, d in ((k, 192), (v, 128)))
+    R.Row(q, kv, vv, torch.arange(n, device="cuda"), torch.arange(n - q_len, n, device="cuda"), 1e7).check(out, lse)
