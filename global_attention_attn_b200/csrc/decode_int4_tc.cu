@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
             rope_cos_sin(pos0 + i / kHalf, p.rope.inv_freq[i % kHalf], &cs[i].x, &cs[i].y);
           if (tid < N) nref[tid] = tid < rows ? INFINITY : -INFINITY;  // (a padding column: weight 0)
           stream_sync();
-        });
+        },
+        [](int) { return true; });
     if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
     fence_proxy_async_smem();
     stream_sync();

@@ -39,12 +39,13 @@ __device__ __forceinline__ void tied(uint32_t* d) {
 // which enter as two fp16 terms (no 16-bit type holds them to the digits of an fp32 log-sum-exp);
 // then a 32-byte row (32-byte swizzle) of the code offset for each of the 6 N columns of sums.
 // q: draft 0's first head of the KV head; row n is head n % 2^g_log of draft n >> g_log, rows from
-// `rows` on are 0.  prepare(): called once the rows' loads are under way; after it `at` is free
-// and cs[draft * 32 + i] holds (cos, sin).  Returns the largest magnitude that this thread stored.
+// `rows` on are 0, and so are those for which counts(n), asked after prepare(), is false.  prepare():
+// called once the rows' loads are under way; after it `at` is free and cs[draft * 32 + i] holds
+// (cos, sin).  Returns the largest magnitude that this thread stored.
 // 8 threads a row: thread r dims 4 r .. 4 r + 3, their rotary partners, and 64 + 16 r .. 64 + 16 r + 15.
-template <int N, int THREADS, int CHUNK, class F>
+template <int N, int THREADS, int CHUNK, class F, class C>
 __device__ __forceinline__ float int4_query_operand(const uint16_t* q, int rows, int g_log, uint32_t at, int tid,
-                                                    const float2* cs, F&& prepare) {
+                                                    const float2* cs, F&& prepare, C&& counts) {
   constexpr int kRows = THREADS / 8, kPasses = (N + kRows - 1) / kRows;
   const int r = tid & 7, G = 1 << g_log;
   uint2 ra[kPasses], rb[kPasses];
@@ -68,6 +69,10 @@ __device__ __forceinline__ float int4_query_operand(const uint16_t* q, int rows,
   for (int i = 0; i < kPasses; ++i) {
     const int n = i * kRows + (tid >> 3);
     if (n >= N) break;  // (warp-uniform)
+    if (!counts(n)) {
+      ra[i] = rb[i] = make_uint2(0, 0);
+      rc[i][0] = rc[i][1] = make_uint4(0, 0, 0, 0);
+    }
     // 8 dims: fields come out of a word as (0, 4), (1, 5), (2, 6), (3, 7), the odd ones times 16 (* 4, / 4)
     auto put = [&](const float* v, int chunk, int unit, bool two) {
       uint32_t hi[4], lo[4];

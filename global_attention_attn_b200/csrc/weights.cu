@@ -202,13 +202,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) weights_kernel(const __grid
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int h = 8 * nb + r0;
+        // (a row that adds nothing may hold NaN or infinities, which no log-sum-exp would cancel: 0)
+        const float on = lse2[i * G + h];
 #pragma unroll
         for (int bb = 0; bb < 2; ++bb) {
           float v[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             // (E4M3 keys come out of ldmatrix as 4 consecutive dims a lane)
-            v[e] = qval(i, h, FMT == MIMO_DTYPE_BF16 ? 16 * kk + 8 * bb + 2 * q4 + e : 16 * kk + 4 * q4 + 2 * bb + e);
+            const float x = qval(i, h, FMT == MIMO_DTYPE_BF16 ? 16 * kk + 8 * bb + 2 * q4 + e : 16 * kk + 4 * q4 + 2 * bb + e);
+            v[e] = on < INFINITY ? x : 0.f;
           }
           if (FMT == MIMO_DTYPE_BF16 && kk >= 4) {
             r[2 * nb + bb] = pack2_bf16(v[0], v[1]);

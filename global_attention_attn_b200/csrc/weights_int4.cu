@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(kWork + 32, 1) weights_int4_kernel(const __gri
             lse2[threadIdx.x] = -l;  // (added to the logits)
           }
           all_sync();
-        });
+        },
+        // (a row that adds nothing may hold NaN or infinities, which no log-sum-exp would cancel)
+        [&](int n) { return lse2[n] != -INFINITY; });
     if (amax > kF16Max) atomicOr(p.status, MIMO_STATUS_RANGE);
     fence_proxy_async_smem();
     all_sync();

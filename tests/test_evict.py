@@ -485,3 +485,33 @@ def test_new_struct_layouts_match_c(tmp_path):
     for py in structs.values():
         want += [C.sizeof(py)] + [getattr(py, f).offset for f, _ in py._fields_]
     assert got == want
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [BF16, E4M3, INT4])
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_weights_of_a_query_row_without_a_number(fmt, q_len):
+    """A query row of NaN or infinities, whose log-sum-exp is no number: it adds nothing, the other rows
+    what they add without it, bit for bit."""
+    g, r = gen(26), np.random.default_rng(26)
+    lens = [900, 131]
+    table, pages = R.table_of(lens, r)
+    k, v, kd, vd = R.random_cache(fmt, pages, g)
+    q = torch.randn((2 * q_len, 64, 192), generator=g, device="cuda").bfloat16()
+    kw = dict(max_seq_len=900, num_kv_heads=4, rope_base=1e7, k_cache=k, block_table=table, num_pages=pages, cache_dtype=fmt,
+              k_dequant=kd, q_len=q_len)
+    _, lse = M.mimo_attn_decode(q, R.i32(lens), window=0, cache_kind=PAGED, v_cache=v, v_dequant=vd, **kw)
+    before = torch.rand((2, 4, 900), generator=g, device="cuda")
+    M.status_poll()
+
+    def run(q, lse):
+        return M.mimo_attn_weights(q, lse, before.clone(), R.i32(lens), **kw)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for what in (slice(None), slice(0, 1), slice(100, 101)):
+            q2, l2 = q.clone(), lse.clone()
+            q2[0, 5, what] = bad          # head 5: KV head 0
+            q2[q_len, 40, what] = bad     # head 40: KV head 2
+            l2[0, 5], l2[q_len, 40] = float("nan"), float("inf")
+            got, want = run(q2, l2), run(q, l2)
+            assert torch.isfinite(got).all() and torch.equal(got, want)
+    assert M.status_poll() in (0, M.MIMO_STATUS_RANGE)
