@@ -30,6 +30,11 @@ __device__ __forceinline__ float key_score(uint32_t k) { return __uint_as_float(
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// The keys that a CTA's registers (8 steps of its threads) leave over of the most slots that a CTA gets:
+// an eighth of the longest row, or 65536.
+constexpr int kMaxRestBytes = 4 * (65536 - 8 * 4 * 1024);
+static_assert(4 * (MIMO_SELECT_MAX_SLOTS / 8 - 8 * 4 * 512) <= kMaxRestBytes, "512 threads, 8 CTAs");
+
 constexpr int kBins = 2048;  // 11, 11 and 10 bits a pass
 constexpr int kBinThreads = kBins / 4;  // a thread's bins are one 16-byte read
 
@@ -288,7 +293,9 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t s) {
   auto kernel = threads == 1024 ? select_kernel<1024, 8> : (steps <= 2 ? select_kernel<512, 2> : select_kernel<512, 8>);
   const size_t bytes = steps <= 8 ? 0 : size_t(steps - 8) * 16 * threads;
   if (bytes > 0) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    // (the attribute is the kernel's, not the launch's: always the same value, as another host thread may
+    // be between its own two calls)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRestBytes);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

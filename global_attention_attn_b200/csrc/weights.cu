@@ -26,6 +26,7 @@ namespace mimo {
 namespace {
 
 constexpr int kTile = 32, kMaxWarps = 8, kStages = 2;
+constexpr int kMaxSmem = 232448;  // of a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int FMT>
@@ -334,9 +335,11 @@ int smem_of(int warps, int q_len, int hkv) {
 template <int FMT, int NB>
 cudaError_t launch_weights_fmt(const WeightsParams& p, int sms, cudaStream_t s) {
   int warps = kMaxWarps;  // as many as their stages fit beside the drafts' fragments
-  while (smem_of<FMT>(warps, p.q_len, p.hkv) > 232448) --warps;
+  while (smem_of<FMT>(warps, p.q_len, p.hkv) > kMaxSmem) --warps;
   const int bytes = smem_of<FMT>(warps, p.q_len, p.hkv);
-  cudaError_t e = cudaFuncSetAttribute(weights_kernel<FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // (the attribute is the kernel's, not the launch's: always the same value, as another host thread may be
+  // between its own two calls)
+  cudaError_t e = cudaFuncSetAttribute(weights_kernel<FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
   const long long tiles = ((long long)p.max_seq_len + kTile - 1) / kTile * p.batch * p.hkv;
   weights_kernel<FMT, NB><<<int(tiles < sms ? tiles : sms), warps * 32, bytes, s>>>(p);

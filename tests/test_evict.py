@@ -515,3 +515,74 @@ def test_weights_of_a_query_row_without_a_number(fmt, q_len):
             got, want = run(q2, l2), run(q, l2)
             assert torch.isfinite(got).all() and torch.equal(got, want)
     assert M.status_poll() in (0, M.MIMO_STATUS_RANGE)
+
+
+def _from_two_threads(fn, calls, times):
+    """Return codes of a C entry point called over and over from a host thread per argument struct, each
+    on a stream of its own."""
+    import threading
+    codes = [set() for _ in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    start = threading.Barrier(len(calls))
+
+    def work(args, stream, seen):
+        ref, handle = C.byref(args), stream.cuda_stream
+        start.wait()
+        for _ in range(times):
+            seen.add(fn(ref, handle))
+    threads = [threading.Thread(target=work, args=x) for x in zip(calls, streams, codes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return codes
+
+
+@gpu
+def test_select_from_two_host_threads():
+    """Rows whose kernels take different amounts of shared memory, selected at the same time."""
+    calls, sets = [], []
+    for n in (390000, 150000):
+        scores = torch.rand((1, 4, n), generator=gen(n), device="cuda")
+        idx, counts, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((1, 4, 500), (1,), (1,)))
+        lens.fill_(n)
+        a = M.MimoSelectArgs()
+        a.num_seqs, a.num_kv_heads, a.score_stride, a.max_seq_len, a.keep = 1, 4, n, n, 500
+        a.scores, a.seq_lens, a.idx, a.counts = (t.data_ptr() for t in (scores, lens, idx, counts))
+        calls.append(a)
+        sets.append((scores, lens, idx, counts, select_ref(scores, [n], 500, 0, 0)))
+    torch.cuda.synchronize()
+    assert _from_two_threads(M.lib().mimo_kv_select, calls, 20000) == [{M.MIMO_OK}] * 2
+    for _, _, idx, _, want in sets:
+        assert torch.equal(idx.cpu(), want)
+    assert M.status_poll() == 0
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+def test_weights_from_two_host_threads(fmt):
+    """One token and eight drafts: other amounts of shared memory of the same kernel."""
+    g = gen(27)
+    k, _, kd, _ = R.random_cache(fmt, 2, g)
+    table, lens, calls, sets = R.i32([[0, 1]]), R.i32([200]), [], []
+    for q_len in (1, 8):
+        q = torch.randn((q_len, 64, 192), generator=g, device="cuda").bfloat16()
+        lse, scores = torch.full((q_len, 64), 5.0, device="cuda"), torch.zeros((1, 4, 256), device="cuda")
+        a = M.MimoWeightsArgs()
+        a.layer = M.make_layer(4, 1e7, 0)
+        a.batch, a.q_len, a.max_seq_len, a.score_stride, a.max_pages, a.num_pages, a.cache_dtype = 1, q_len, 200, 256, 2, 2, fmt
+        a.q, a.lse, a.seq_lens, a.k_cache, a.block_table, a.scores = (t.data_ptr() for t in (q, lse, lens, k, table, scores))
+        a.k_dequant = kd.data_ptr() if fmt == E4M3 else None
+        calls.append(a)
+        sets.append((q, lse, scores))
+    torch.cuda.synchronize()
+    assert _from_two_threads(M.lib().mimo_attn_weights, calls, 20000) == [{M.MIMO_OK}] * 2
+    assert M.status_poll() == 0
+
+
+@gpu
+def test_weights_ignore_what_lies_behind_e4m3():
+    def spoil(k, table):
+        k[int(table[0, 1]), 40:] = 0x7F  # NaN
+    check_weights([168], E4M3, seed=23, edit=spoil)
