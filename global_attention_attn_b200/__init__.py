@@ -182,6 +182,26 @@ def _stream(stream, t):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(like, shape, dtype, stream):
+    """A tensor for a call on `stream`, on the device of `like`.  Memory made for another stream than
+    the current one is that stream's: a block of the current stream's may still be read there when
+    the call runs, and one given back to it would be handed out again before the call has run.  The
+    current stream is noted as a user of it, so that its reads are waited for too."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    here = torch.cuda.current_stream()
+    handle = _stream(stream, like)
+    if handle == here.cuda_stream:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):  # (0 and 1 are the legacy default stream)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(here)
+    return t
+
+
 def make_layer(num_kv_heads: int, rope_base: float, window: int, sink=None, softmax_scale: float = SOFTMAX_SCALE,
                v_scale: float = V_SCALE) -> MimoLayer:
     L = MimoLayer()
@@ -231,12 +251,12 @@ def mimo_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, *, num_kv_heads: int,
     num_seqs = cu_seqlens_q.shape[0] - 1
     total_k = 0 if k is None else k.shape[0]
     if out is None:
-        out = torch.empty((total_q, NUM_Q_HEADS, HEAD_DIM_V), dtype=torch.bfloat16, device=q.device)
+        out = _new(q, (total_q, NUM_Q_HEADS, HEAD_DIM_V), torch.bfloat16, stream)
     if lse is None and with_lse:
-        lse = torch.empty((total_q, NUM_Q_HEADS), dtype=torch.float32, device=q.device)
+        lse = _new(q, (total_q, NUM_Q_HEADS), torch.float32, stream)
     need = prefill_workspace_size(num_seqs, total_q, total_k, num_kv_heads, cache_kind)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(q, (need,), torch.uint8, stream)
     a = MimoPrefillArgs()
     a.layer = make_layer(num_kv_heads, rope_base, window, sink, softmax_scale, v_scale)
     a.num_seqs, a.total_q, a.total_k = num_seqs, total_q, total_k
@@ -276,13 +296,13 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
         raise ValueError("q holds batch * q_len rows")
     B = rows // q_len
     if out is None:
-        out = q.new_empty((rows, NUM_Q_HEADS, HEAD_DIM_V), dtype=torch.bfloat16)
+        out = _new(q, (rows, NUM_Q_HEADS, HEAD_DIM_V), torch.bfloat16, stream)
     if lse is None and with_lse:
-        lse = q.new_empty((rows, NUM_Q_HEADS), dtype=torch.float32)
+        lse = _new(q, (rows, NUM_Q_HEADS), torch.float32, stream)
     if workspace is None:
         need = decode_workspace_size(B, max_seq_len, num_kv_heads, window, q_len, cache_dtype, cache_kind)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _new(q, (need,), torch.uint8, stream)
     a = MimoDecodeArgs()
     a.layer = make_layer(num_kv_heads, rope_base, window, sink, softmax_scale, v_scale)
     a.batch, a.max_seq_len = B, int(max_seq_len)
@@ -387,15 +407,15 @@ def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int
         raise ValueError("scores is a contiguous float32 [num_seqs, num_kv_heads, slots] tensor")
     n, h, slots = scores.shape
     if idx is None:
-        idx = scores.new_empty((n, h, keep), dtype=torch.int32)
+        idx = _new(scores, (n, h, keep), torch.int32, stream)
     else:
         _check32(idx, n * h * keep, "idx")
     if counts is None:
-        counts = scores.new_empty((n,), dtype=torch.int32)
+        counts = _new(scores, (n,), torch.int32, stream)
     else:
         _check32(counts, n, "counts")
     if scores_out is None:
-        scores_out = scores.new_empty((n, h, keep), dtype=torch.float32)
+        scores_out = _new(scores, (n, h, keep), torch.float32, stream)
     else:
         _check32(scores_out, n * h * keep, "scores_out")
     a = MimoSelectArgs()

@@ -543,3 +543,52 @@ def test_decode_one_dominant_key_over_a_flat_tail(q_len):
     assert M.status_poll() == 0
     kv, vv = (R.pages_of(R.slots_of(c, R.INT4, d), table[0], n) for c, d in ((k, 192), (v, 128)))
     R.Row(q, kv, vv, torch.arange(n, device="cuda"), torch.arange(n - q_len, n, device="cuda"), 1e7).check(out, lse)
+
+
+@gpu
+def test_memory_made_for_another_stream(monkeypatch):
+    """What a call with stream= allocates belongs to that stream: no block of it is handed out on the
+    current stream while the call may still run, and none that the current stream may still use is
+    taken for it."""
+    g = gen(71)
+    side, made = torch.cuda.Stream(), []
+    table, pages = R.table_of([5000], np.random.default_rng(71))
+    k, v, _, _ = R.random_cache(R.INT4, pages, g)
+    q = torch.randn((1, 64, 192), generator=g, device="cuda").bfloat16()
+    lens = R.i32([5000])
+    kw = dict(max_seq_len=5000, num_kv_heads=4, rope_base=1e7, window=0, cache_kind=PAGED, k_cache=k, v_cache=v,
+              block_table=table, num_pages=pages, cache_dtype=M.MIMO_DTYPE_INT4)
+    want = M.mimo_attn_decode(q, lens, **kw)
+    need = M.decode_workspace_size(1, 5000, 4, 0, 1, M.MIMO_DTYPE_INT4)
+    scores = torch.rand((1, 4, 5000), generator=g, device="cuda")
+    picked = M.mimo_kv_select(scores, lens, max_seq_len=5000, keep=300)
+    torch.cuda.synchronize()
+    sizes = [need, q.numel() // 192 * 128 * 2, 64 * 4, 300 * 4 * 4]
+
+    def current_blocks():  # blocks that the current stream has just given back
+        x = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes]
+        return {t.data_ptr() for t in x}
+    plain, new_empty = torch.empty, torch.Tensor.new_empty
+
+    def note(f):
+        def wrapped(*a, **k):
+            t = f(*a, **k)
+            made.append(t.data_ptr())
+            return t
+        return wrapped
+    for stream in (side, side.cuda_stream):
+        free = current_blocks()
+        made.clear()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)  # some 25 ms
+        with monkeypatch.context() as m:
+            m.setattr(torch, "empty", note(plain))
+            m.setattr(torch.Tensor, "new_empty", note(new_empty))
+            got = M.mimo_attn_decode(q, lens, stream=stream, **kw)
+            sel = M.mimo_kv_select(scores, lens, max_seq_len=5000, keep=300, stream=stream)
+        assert len(made) >= 6 and not free & set(made)
+        assert not current_blocks() & set(made)
+        side.synchronize()
+        for a, b in zip(got + sel, want + picked):
+            assert torch.equal(a, b)
+    assert M.status_poll() == 0
