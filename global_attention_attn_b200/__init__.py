@@ -172,11 +172,12 @@ def _ptr(t):
 
 
 def _stream(stream, t):
-    """Handle of the stream that a call on tensor t goes to."""
+    """Handle of the stream that a call on tensor t goes to.  The library works on the current device:
+    tensors of another one are refused, whatever the stream."""
+    import torch
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
     if stream is None:
-        import torch
-        if t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {t.device}, which is not the current device")
         # (the handle alone: making a torch.cuda.Stream of it takes 3 us, a quarter of a short decode)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)

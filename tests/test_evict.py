@@ -586,3 +586,13 @@ def test_weights_ignore_what_lies_behind_e4m3():
     def spoil(k, table):
         k[int(table[0, 1]), 40:] = 0x7F  # NaN
     check_weights([168], E4M3, seed=23, edit=spoil)
+
+
+def test_tensors_of_another_device_are_refused_on_any_stream(monkeypatch):
+    other = type("T", (), dict(is_cuda=True, device=torch.device("cuda", 1)))()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for stream in (None, 0, 12345678, type("S", (), dict(cuda_stream=4096))()):
+        with pytest.raises(ValueError, match="current device"):
+            M._stream(stream, other)
+    here = type("T", (), dict(is_cuda=True, device=torch.device("cuda", 0)))()
+    assert M._stream(12345678, here) == 12345678
