@@ -226,9 +226,8 @@ size_t decode_workspace(int batch, int q_len, int max_seq_len, int window) {
 }
 
 // Segments of a 4-bit decode's workers, and the tile table its combine reads.
-size_t decode4_workspace(const Decode4Plan& d, int batch) {
-  if (d.no_pieces) return 0;
-  const size_t rows = 2 * size_t(d.workers) * d.n_blocks * 16;
+size_t decode4_workspace(int workers, int n_blocks, int batch) {
+  const size_t rows = 2 * size_t(workers) * n_blocks * 16;
   return round256(rows * kDv * 4) + round256(rows * 2 * 4) +
          round256((size_t(batch < kMaxTableBatch ? batch : kMaxTableBatch) + 1) * 8);
 }
@@ -246,7 +245,7 @@ int decode_int4(const char* fn, const mimo_decode_args* a, int q_len, int ring_s
   Decode4Plan plan = decode4_plan(a->batch < kMaxTableBatch ? a->batch : kMaxTableBatch, hkv, q_len,
                                   ring ? ring_slots : decode_unit_keys(a->max_seq_len, a->layer.window, q_len), ring,
                                   d.sms < kI4Sms ? d.sms : kI4Sms);
-  while (!plan.whole_units && plan.workers > 1 && decode4_workspace(plan, a->batch) > room) --plan.workers;
+  while (!plan.whole_units && plan.workers > 1 && decode4_workspace(plan.workers, plan.n_blocks, a->batch) > room) --plan.workers;
   const long tiles = a->max_seq_len / kPage + 2L;
   if (!ring && (long(a->num_pages) * hkv > INT_MAX || tiles * (a->batch < kMaxTableBatch ? a->batch : kMaxTableBatch) * hkv > INT_MAX))
     return fail(MIMO_ERR_UNSUPPORTED, "%s: num_pages * num_kv_heads, or the pages of max_seq_len in all, pass 2^31", fn);
@@ -449,9 +448,9 @@ size_t mimo_attn_decode_int4_workspace_size(int batch, int q_len, int max_seq_le
   if (batch <= 0 || max_seq_len <= 0 || q_len < 1 || q_len > MIMO_MAX_DRAFTS || (num_kv_heads != 8 && num_kv_heads != 4) ||
       window < 0 || cache_kind != MIMO_CACHE_PAGED)
     return 0;
-  return decode4_workspace(decode4_plan(batch < kMaxTableBatch ? batch : kMaxTableBatch, num_kv_heads, q_len,
-                                        decode_unit_keys(max_seq_len, window, q_len), false, kI4Sms),
-                           batch);
+  const Decode4Plan d = decode4_plan(batch < kMaxTableBatch ? batch : kMaxTableBatch, num_kv_heads, q_len,
+                                     decode_unit_keys(max_seq_len, window, q_len), false, kI4Sms);
+  return d.no_pieces ? 0 : decode4_workspace(d.max_workers, d.n_blocks, batch);
 }
 
 int mimo_kv_append(const mimo_append_args* a, void* stream) {

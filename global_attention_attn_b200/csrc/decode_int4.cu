@@ -559,6 +559,9 @@ Decode4Plan decode4_plan(int batch, int hkv, int q_len, int unit_keys, bool ring
   const long long most = d.whole_units ? units : units * tiles;
   const long long all = (long long)sms * d.groups / d.split;
   d.workers = int(most < all ? most : all);
+  // A batch that is cut has more workers than a larger one of whole units; a buffer for the larger one
+  // has to serve it.  Units that no batch cuts leave the tile table alone.
+  d.max_workers = unit_keys <= 512 ? 0 : int(units * tiles < all ? units * tiles : all);
   return d;
 }
 

@@ -109,7 +109,8 @@ struct Decode4Params {
 struct Decode4Plan {
   int tc;
   int tile, n_blocks, nc, groups, split, stages, workers, whole_units;
-  int no_pieces;  // units so short that no batch of them is cut: no workspace
+  int no_pieces;    // no workspace is asked for: rings, units of at most two tiles
+  int max_workers;  // what the workspace is sized for: never less for a larger batch or longer units
 };
 
 // Attention weights per cached slot (weights.cu).

@@ -296,7 +296,8 @@ MIMO_API size_t mimo_attn_verify_workspace_size(int batch, int q_len, int max_se
                                                 int window);
 
 /* The same for a 4-bit cache (MIMO_DTYPE_INT4) of the given kind; at most 20 MB, whatever the
- * batch.  0 for sizes that a call refuses.  Calls that may run at the same time (on two streams, in
+ * batch, and never less for a larger batch or max_seq_len: a buffer for the largest serves every
+ * call.  0 for sizes that a call refuses.  Calls that may run at the same time (on two streams, in
  * two graphs) need a workspace each. */
 MIMO_API size_t mimo_attn_decode_int4_workspace_size(int batch, int q_len, int max_seq_len, int num_kv_heads,
                                                      int window, int cache_kind);

@@ -592,3 +592,29 @@ def test_memory_made_for_another_stream(monkeypatch):
         for a, b in zip(got + sel, want + picked):
             assert torch.equal(a, b)
     assert M.status_poll() == 0
+
+
+@pytest.mark.parametrize("hkv", [4, 8])
+def test_workspace_size_never_shrinks(hkv):
+    """A buffer for the largest batch and context serves every smaller one."""
+    size = M.lib().mimo_attn_decode_int4_workspace_size
+    for q_len in (1, 2, 4, 8):
+        for n in (257, 300, 512, 513, 700, 1000, 1024, 1025, 5000, 100000):
+            over_batch = [size(b, q_len, n, hkv, 0, PAGED) for b in list(range(1, 160)) + [500, 1023, 1024, 1025, 5000]]
+            assert over_batch == sorted(over_batch) and over_batch[0] > 0
+        for b in (1, 7, 24, 25, 64, 300):
+            over_keys = [size(b, q_len, n, hkv, 0, PAGED) for n in range(q_len, 3000, 7)]
+            assert over_keys == sorted(over_keys)
+    # units of up to 512 keys are never cut: no pieces to hold
+    assert size(64, 1, 512, 4, 0, PAGED) < 1024
+
+
+@gpu
+@pytest.mark.parametrize("q_len", [1, 4])
+def test_decode_with_a_buffer_for_a_larger_batch(q_len):
+    """One buffer, sized for the largest batch, through batches on either side of whole and cut units."""
+    ws = torch.empty(M.decode_workspace_size(48, 1000, 4, 0, q_len, M.MIMO_DTYPE_INT4), dtype=torch.uint8, device="cuda")
+    for B in (48, 25, 24, 13, 12, 1):
+        lens = [int(x) for x in np.random.default_rng(B).integers(q_len, 1001, B)]
+        check_paged(lens, q_len=q_len, seed=72, max_seq_len=1000, rows=[0, B - 1],
+                    call=lambda *a, **kw: M.mimo_attn_decode(*a, workspace=ws, **kw))
