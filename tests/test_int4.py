@@ -615,6 +615,6 @@ def test_decode_with_a_buffer_for_a_larger_batch(q_len):
     """One buffer, sized for the largest batch, through batches on either side of whole and cut units."""
     ws = torch.empty(M.decode_workspace_size(48, 1000, 4, 0, q_len, M.MIMO_DTYPE_INT4), dtype=torch.uint8, device="cuda")
     for B in (48, 25, 24, 13, 12, 1):
-        lens = [int(x) for x in np.random.default_rng(B).integers(q_len, 1001, B)]
+        lens = [1000] + [int(x) for x in np.random.default_rng(B).integers(q_len, 1001, B - 1)]  # (8 pages)
         check_paged(lens, q_len=q_len, seed=72, max_seq_len=1000, rows=[0, B - 1],
                     call=lambda *a, **kw: M.mimo_attn_decode(*a, workspace=ws, **kw))
