@@ -203,6 +203,23 @@ def _new(like, shape, dtype, stream):
     return t
 
 
+def _check32(t, size: int, name: str):
+    if t.numel() != size or t.element_size() != 4 or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous 32-bit tensor of {size} elements")
+
+
+def _check_input(t, size: int, name: str, like, dtype: str = "int32"):
+    """A small input, which the kernels read `size` elements of."""
+    if str(t.dtype) != "torch." + dtype or t.numel() < size or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name} is a contiguous {dtype} tensor of {size} elements on {like.device}")
+
+
+def _check_table(t, rows: int, name: str, like):
+    if t.ndim != 2:
+        raise ValueError(f"{name} is a contiguous int32 [{rows}, pages] tensor")
+    _check_input(t, rows * t.shape[1], name, like)
+
+
 def make_layer(num_kv_heads: int, rope_base: float, window: int, sink=None, softmax_scale: float = SOFTMAX_SCALE,
                v_scale: float = V_SCALE) -> MimoLayer:
     L = MimoLayer()
@@ -296,6 +313,8 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
     if rows % q_len:
         raise ValueError("q holds batch * q_len rows")
     B = rows // q_len
+    if positions is not None:
+        _check_input(positions, B, "positions", q)
     if out is None:
         out = _new(q, (rows, NUM_Q_HEADS, HEAD_DIM_V), torch.bfloat16, stream)
     if lse is None and with_lse:
@@ -353,6 +372,8 @@ def mimo_kv_append(k_new, v_new, pos, seq_idx, *, rope_base: float, cache_kind: 
     an E4M3 cache (cache_dtype) quantises with the per-KV-head scales k_dequant / v_dequant, a
     4-bit cache with scales of its own.  ring_slots: slots per sequence of a ring cache (0 =
     128).  slots: int32 [tokens] cache slot of each token where it is not pos (paged caches)."""
+    if slots is not None:
+        _check_input(slots, k_new.shape[0], "slots", k_new)
     a = MimoAppendArgs()
     a.num_tokens, a.num_kv_heads = k_new.shape[0], k_new.shape[1]
     a.head_dim_qk, a.head_dim_v, a.rope_dim, a.rope_base = HEAD_DIM_QK, HEAD_DIM_V, ROPE_DIM, float(rope_base)
@@ -380,6 +401,11 @@ def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_head
     if (scores.ndim != 3 or scores.shape[0] != B or scores.shape[1] != num_kv_heads or not scores.is_contiguous()
             or scores.element_size() != 4):
         raise ValueError("scores is a contiguous float32 [batch, num_kv_heads, slots] tensor")
+    _check_input(lse, q.shape[0] * NUM_Q_HEADS, "lse", q, "float32")
+    _check_input(seq_lens, B, "seq_lens", q)
+    if positions is not None:
+        _check_input(positions, B, "positions", q)
+    _check_table(block_table, B, "block_table", q)
     a = MimoWeightsArgs()
     a.layer = make_layer(num_kv_heads, rope_base, 0, None, softmax_scale, 1.0)
     a.batch, a.q_len, a.max_seq_len = B, int(q_len), int(max_seq_len)
@@ -392,11 +418,6 @@ def mimo_attn_weights(q, lse, scores, seq_lens, *, max_seq_len: int, num_kv_head
     return scores
 
 
-def _check32(t, size: int, name: str):
-    if t.numel() != size or t.element_size() != 4 or not t.is_contiguous():
-        raise ValueError(f"{name} is a contiguous 32-bit tensor of {size} elements")
-
-
 def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int = 0, first: int = 0, idx=None,
                    counts=None, scores_out=None, stream=None):
     """The slots that stay of every (sequence, KV head): the first `first`, the last `recent`, and the
@@ -407,6 +428,7 @@ def mimo_kv_select(scores, seq_lens, *, max_seq_len: int, keep: int, recent: int
     if scores.ndim != 3 or not scores.is_contiguous() or scores.element_size() != 4:
         raise ValueError("scores is a contiguous float32 [num_seqs, num_kv_heads, slots] tensor")
     n, h, slots = scores.shape
+    _check_input(seq_lens, n, "seq_lens", scores)
     if idx is None:
         idx = _new(scores, (n, h, keep), torch.int32, stream)
     else:
@@ -439,6 +461,9 @@ def mimo_kv_gather(k_src, v_src, block_table_src, k_dst, v_dst, block_table_dst,
     a.num_seqs, a.num_kv_heads = block_table_src.shape[0], num_kv_heads
     if block_table_dst.shape[0] != a.num_seqs or counts.shape[0] != a.num_seqs:
         raise ValueError("both block tables and counts have a row per sequence")
+    _check_input(counts, a.num_seqs, "counts", k_src)
+    _check_table(block_table_src, a.num_seqs, "block_table_src", k_src)
+    _check_table(block_table_dst, a.num_seqs, "block_table_dst", k_src)
     if idx is not None and (idx.ndim != 3 or tuple(idx.shape[:2]) != (a.num_seqs, num_kv_heads) or not idx.is_contiguous()
                             or idx.element_size() != 4):
         raise ValueError("idx is a contiguous int32 [num_seqs, num_kv_heads, n] tensor")

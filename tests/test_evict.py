@@ -596,3 +596,40 @@ def test_tensors_of_another_device_are_refused_on_any_stream(monkeypatch):
             M._stream(stream, other)
     here = type("T", (), dict(is_cuda=True, device=torch.device("cuda", 0)))()
     assert M._stream(12345678, here) == 12345678
+
+
+def test_python_refusals_of_index_tensors():
+    """The small tensors of the eviction calls and what decode and append take for evicted caches: a
+    64-bit, short or strided one is refused, not read as something else."""
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    s, n, q = torch.zeros((2, 4, 64)), torch.ones(2, dtype=torch.int32), torch.zeros((4, 64, 192), dtype=torch.bfloat16)
+    wide = torch.zeros(4, dtype=torch.int32)[::2]
+    bad32 = (n.long(), n[:1], wide, n.float())
+    wkw = dict(max_seq_len=32, num_kv_heads=4, rope_base=1e7, k_cache=s, block_table=i(2, 1), num_pages=1, q_len=2, stream=0)
+    for bad in bad32:
+        with pytest.raises(ValueError, match="seq_lens"):
+            M.mimo_kv_select(s, bad, max_seq_len=32, keep=8, stream=0)
+        with pytest.raises(ValueError, match="seq_lens"):
+            M.mimo_attn_weights(q, torch.zeros((4, 64)), s, bad, **wkw)
+        with pytest.raises(ValueError, match="positions"):
+            M.mimo_attn_weights(q, torch.zeros((4, 64)), s, n, positions=bad, **wkw)
+        with pytest.raises(ValueError, match="positions"):
+            M.mimo_attn_decode(q, n, max_seq_len=32, num_kv_heads=4, rope_base=1e7, window=0, cache_kind=PAGED, k_cache=s,
+                               v_cache=s, block_table=i(2, 1), num_pages=1, q_len=2, positions=bad, stream=0)
+        with pytest.raises(ValueError, match="slots"):
+            M.mimo_kv_append(torch.zeros((2, 4, 192)).bfloat16(), torch.zeros((2, 4, 128)).bfloat16(), n, n, rope_base=1e7,
+                             cache_kind=PAGED, k_cache=s, v_cache=s, num_seqs=2, block_table=i(2, 1), num_pages=1, slots=bad,
+                             stream=0)
+    for bad in (n.long(), wide, n.float()):
+        with pytest.raises(ValueError, match="counts"):
+            M.mimo_kv_gather(s, s, i(2, 1), s, s, i(2, 1), bad, num_kv_heads=4, num_pages=1, num_pages_out=1, stream=0)
+    for bad in (torch.zeros((2, 64)), torch.zeros((4, 64)).double(), torch.zeros((4, 128))[:, ::2], i(4, 64)):
+        with pytest.raises(ValueError, match="lse"):
+            M.mimo_attn_weights(q, bad, s, n, **wkw)
+    for bad in (i(2, 1).long(), i(1, 1), i(2, 4)[:, ::2], i(2)):
+        with pytest.raises(ValueError, match="block_table"):
+            M.mimo_attn_weights(q, torch.zeros((4, 64)), s, n, **{**wkw, "block_table": bad})
+    for bad in (i(2, 1).long(), i(2, 4)[:, ::2]):
+        for tables in ((bad, i(2, 1)), (i(2, 1), bad)):
+            with pytest.raises(ValueError, match="block_table"):
+                M.mimo_kv_gather(s, s, tables[0], s, s, tables[1], n, num_kv_heads=4, num_pages=1, num_pages_out=1, stream=0)
