@@ -337,9 +337,9 @@ __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_const
   __shared__ long from[kMoveSlots];  // source entry (page * 128 + slot) of each destination slot, or -1
   const int s = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * kMoveSlots, tid = threadIdx.x;
   int count = p.counts[s];
-  if (count > p.max_count) {
+  if (count < 0 || count > p.max_count) {
     if (g == 0 && blockIdx.x == 0 && tid == 0) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-    count = p.max_count;
+    count = min(count, p.max_count);  // (below 0: nothing to move)
   }
   const int n = min(kMoveSlots, count - j0);
   if (n <= 0) return;

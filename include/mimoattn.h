@@ -453,7 +453,7 @@ MIMO_API int mimo_kv_select(const mimo_select_args* args, void* stream);
  * No page may be both read and written by one call, nor written for two sequences: evict into fresh
  * pages and release the old ones (pages shared between sequences stay whole).  Destination slots from counts[s] on are
  * left as they were.  A slot or page outside its table or cache sets MIMO_STATUS_BAD_INDEX and
- * is skipped; counts[s] above max_count is cut to it and reported.
+ * is skipped; counts[s] above max_count is cut to it, one below 0 counts as 0, both reported.
  */
 typedef struct {
   int num_seqs;

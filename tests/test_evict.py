@@ -633,3 +633,14 @@ def test_python_refusals_of_index_tensors():
         for tables in ((bad, i(2, 1)), (i(2, 1), bad)):
             with pytest.raises(ValueError, match="block_table"):
                 M.mimo_kv_gather(s, s, tables[0], s, s, tables[1], n, num_kv_heads=4, num_pages=1, num_pages_out=1, stream=0)
+
+
+@gpu
+def test_gather_reports_a_negative_count():
+    g = gen(10)
+    k, v, _, _ = R.random_cache(BF16, 3, g)
+    ko, vo = _empty(BF16, 2, 4)
+    M.mimo_kv_gather(k, v, R.i32([[0], [1]]), ko, vo, R.i32([[0], [1]]), R.i32([-1, 2]), num_kv_heads=4, num_pages=3,
+                     num_pages_out=2)
+    assert M.status_poll() == M.MIMO_STATUS_BAD_INDEX
+    assert not ko[0].any() and torch.equal(ko[1, :2], k[1, :2]) and not ko[1, 2:].any()
