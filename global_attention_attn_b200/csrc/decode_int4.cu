@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
   if (warp == kWarps - 1) {
     const int ring_tiles = (p.ring_slots + kTile - 1) / kTile;
     tile_table(tbl, p.batch, lane, [&](int s) {
-      const bool bad = p.seq_lens[s] < p.q_len;
-      if (blockIdx.x == 0 && bad) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
-      return bad ? 0 : ring_tiles;
+      const int ctx = p.seq_lens[s];
+      if (blockIdx.x == 0 && (ctx < p.q_len || ctx > p.max_seq_len)) atomicOr(p.status, MIMO_STATUS_BAD_INDEX);
+      return ctx < p.q_len ? 0 : ring_tiles;
     });
   }
   __syncthreads();

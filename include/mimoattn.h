@@ -248,7 +248,7 @@ MIMO_API int mimo_attn_prefill_stall_test(const mimo_prefill_args* args, void* s
  * combine pass.  Either way the split-KV workspace is the one the size queries give.  4-bit
  * caches (MIMO_DTYPE_INT4) have decode kernels and a workspace size query of their own
  * (mimo_attn_decode_int4_workspace_size); there a seq_lens above max_seq_len is always
- * reported, and its keys from max_seq_len on are not attended.
+ * reported; over pages its keys from max_seq_len on are not attended (a ring's window is).
  *
  * positions (device int32 [batch], or NULL): the rotary position of each sequence's last
  * query token, where it is not seq_lens[s] - 1: after an eviction the cache holds fewer

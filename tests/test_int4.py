@@ -618,3 +618,18 @@ def test_decode_with_a_buffer_for_a_larger_batch(q_len):
         lens = [1000] + [int(x) for x in np.random.default_rng(B).integers(q_len, 1001, B - 1)]  # (8 pages)
         check_paged(lens, q_len=q_len, seed=72, max_seq_len=1000, rows=[0, B - 1],
                     call=lambda *a, **kw: M.mimo_attn_decode(*a, workspace=ws, **kw))
+
+
+@gpu
+def test_decode_ring_reports_lengths_above_the_bound():
+    """As over pages; the rows are those of a call with a bound that holds."""
+    g = gen(55)
+    k, v, _, _ = R.random_cache(R.INT4, 3, g, 8, 128)
+    q = torch.randn((3, 64, 192), generator=g, device="cuda").bfloat16()
+    run = lambda n: M.mimo_attn_decode(q, R.i32([50, 301, 200]), max_seq_len=n, num_kv_heads=8, rope_base=1e4, window=128,
+                                       cache_kind=RING, k_cache=k, v_cache=v, cache_dtype=M.MIMO_DTYPE_INT4)
+    a = run(301)
+    assert M.status_poll() == 0
+    b = run(300)
+    assert M.status_poll() == M.MIMO_STATUS_BAD_INDEX
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
