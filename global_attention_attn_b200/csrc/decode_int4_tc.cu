@@ -618,8 +618,10 @@ __global__ void __launch_bounds__(Lay<N>::kThreads, 1) decode4_tc_kernel(const _
         }
       }
       if (++vst == Y::kStagesV) vst = 0, ++vph;
-      // (every warp arrives, its own waits being bounded)
-      for (int i = 0; i < 1000000 && !mbar_try_wait_hint(vote, x & 1, 20000); ++i) {
+      // (every warp arrives, whatever became of its waits, and must not be left behind at the barriers
+      // below: a probe takes 4 us, so this gives up after 16 s, beyond the six waits of 2 s that another
+      // warp can have since the last vote; the one that ran out has set the status)
+      for (int i = 0; i < 4000000 && !mbar_try_wait_hint(vote, x & 1, 20000); ++i) {
       }
       if (flag[x & 1] == x + 1) {
         // the references that were passed move to their new maxima, and the sums with them
