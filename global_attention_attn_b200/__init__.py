@@ -345,13 +345,20 @@ def mimo_attn_decode(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_b
 def mimo_attn_decode_noalloc(q, seq_lens, *, max_seq_len: int, num_kv_heads: int, rope_base: float, window: int,
                              cache_kind: int, k_cache, v_cache, out, lse=None, block_table=None, num_pages: int = 0,
                              sink=None, softmax_scale: float = SOFTMAX_SCALE, v_scale: float = V_SCALE, stream=None,
-                             cache_dtype: int = MIMO_DTYPE_BF16, k_dequant=None, v_dequant=None, ring_slots: int = 0):
+                             cache_dtype: int = MIMO_DTYPE_BF16, k_dequant=None, v_dequant=None, ring_slots: int = 0,
+                             q_len: int = 1, positions=None):
     """Decode that allocates nothing (see mimo_attn_decode_noalloc in include/mimoattn.h): the
     caller passes the output buffers; the split-KV partials go to the library's static
-    device scratch (16 MiB), so concurrent calls must not overlap on the GPU."""
+    device scratch (16 MiB), so concurrent calls must not overlap on the GPU.  q_len and positions
+    as for mimo_attn_decode."""
+    if q.shape[0] % q_len:
+        raise ValueError("q holds batch * q_len rows")
+    B = q.shape[0] // q_len
+    if positions is not None:
+        _check_input(positions, B, "positions", q)
     a = MimoDecodeArgs()
     a.layer = make_layer(num_kv_heads, rope_base, window, sink, softmax_scale, v_scale)
-    a.batch, a.max_seq_len = q.shape[0], int(max_seq_len)
+    a.batch, a.max_seq_len = B, int(max_seq_len)
     a.q, a.seq_lens = _ptr(q), _ptr(seq_lens)
     a.cache_kind = cache_kind
     a.k_cache, a.v_cache, a.block_table = _ptr(k_cache), _ptr(v_cache), _ptr(block_table)
@@ -359,7 +366,8 @@ def mimo_attn_decode_noalloc(q, seq_lens, *, max_seq_len: int, num_kv_heads: int
     a.num_pages = num_pages
     a.out, a.lse = _ptr(out), _ptr(lse)
     a.cache_dtype, a.k_dequant, a.v_dequant = cache_dtype, _ptr(k_dequant), _ptr(v_dequant)
-    a.ring_slots = int(ring_slots)
+    a.ring_slots, a.q_len = int(ring_slots), int(q_len)
+    a.positions = _ptr(positions)
     _check(lib().mimo_attn_decode_noalloc(C.byref(a), _stream(stream, q)))
     return out, lse
 

@@ -633,3 +633,22 @@ def test_decode_ring_reports_lengths_above_the_bound():
     b = run(300)
     assert M.status_poll() == M.MIMO_STATUS_BAD_INDEX
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [R.BF16, R.INT4])
+def test_decode_noalloc_drafts_and_positions(fmt):
+    """The call that allocates nothing takes what the other takes: the same rows."""
+    g, r = gen(73), np.random.default_rng(73)
+    lens, pos, q_len = [300, 1200], [9000, 1199], 3
+    table, pages = R.table_of(lens, r)
+    k, v, _, _ = R.random_cache(fmt, pages, g)
+    q = torch.randn((2 * q_len, 64, 192), generator=g, device="cuda").bfloat16()
+    for p in (None, R.i32(pos)):
+        kw = dict(max_seq_len=1200, num_kv_heads=4, rope_base=1e7, window=0, cache_kind=PAGED, k_cache=k, v_cache=v,
+                  block_table=table, num_pages=pages, cache_dtype=fmt, q_len=q_len, positions=p)
+        out, lse = torch.empty((6, 64, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((6, 64), device="cuda")
+        M.mimo_attn_decode_noalloc(q, R.i32(lens), out=out, lse=lse, **kw)
+        want = M.mimo_attn_decode(q, R.i32(lens), **kw)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert M.status_poll() == 0
