@@ -241,8 +241,8 @@ MIMO_API int mimo_attn_prefill_stall_test(const mimo_prefill_args* args, void* s
  * that max_seq_len sizes are not attended (reported as MIMO_STATUS_BAD_INDEX whenever the
  * call has more than one split).
  *
- * Kernels: one token per sequence, a ring cache, an E4M3 cache or a window run the
- * split-KV decode kernel; draft rows (q_len >= 2) of a global layer (4 KV heads, no
+ * Kernels: one token per sequence, a ring cache, an E4M3 cache, a window or `positions` run
+ * the split-KV decode kernel; other draft rows (q_len >= 2) of a global layer (4 KV heads, no
  * window) on a bf16 paged cache run the tensor-core prefill kernel, whose 128-row tile
  * holds the q_len x 16 query rows of one KV head, over page-aligned splits, then the same
  * combine pass.  Either way the split-KV workspace is the one the size queries give.  4-bit
@@ -254,7 +254,9 @@ MIMO_API int mimo_attn_prefill_stall_test(const mimo_prefill_args* args, void* s
  * query token, where it is not seq_lens[s] - 1: after an eviction the cache holds fewer
  * slots than the sequence has tokens, and the keys carry the positions they were appended
  * with.  seq_lens then counts slots, and query row i sees slots 0 .. seq_lens[s] - q_len + i.
- * Paged caches without a window only (MIMO_ERR_INVALID_ARG otherwise).
+ * Paged caches without a window only (MIMO_ERR_INVALID_ARG otherwise).  On a bf16 cache it
+ * moves draft rows to the split-KV kernel: 64 sequences of 4096..65536 keys with 4 drafts take
+ * 2.67 ms there, 1.25 ms on the tensor-core kernel.
  */
 #define MIMO_MAX_DRAFTS 8
 typedef struct {

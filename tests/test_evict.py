@@ -644,3 +644,24 @@ def test_gather_reports_a_negative_count():
                      num_pages_out=2)
     assert M.status_poll() == M.MIMO_STATUS_BAD_INDEX
     assert not ko[0].any() and torch.equal(ko[1, :2], k[1, :2]) and not ko[1, 2:].any()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [BF16, E4M3, INT4])
+@pytest.mark.parametrize("q_len", [2, 4, 8])
+def test_decode_drafts_with_positions(fmt, q_len):
+    """Draft tokens over an evicted cache: slots and rotary positions differ, in every cache format."""
+    g, r = gen(28), np.random.default_rng(28)
+    lens, pos = [200, 3000, 9], [5000, 120000, 8]
+    table, pages = R.table_of(lens, r)
+    k, v, kd, vd = R.random_cache(fmt, pages, g)
+    q = torch.randn((3 * q_len, 64, 192), generator=g, device="cuda").bfloat16()
+    out, lse = M.mimo_attn_decode(q, R.i32(lens), max_seq_len=3000, num_kv_heads=4, rope_base=1e7, window=0, cache_kind=PAGED,
+                                  k_cache=k, v_cache=v, block_table=table, num_pages=pages, cache_dtype=fmt, k_dequant=kd,
+                                  v_dequant=vd, q_len=q_len, positions=R.i32(pos))
+    assert M.status_poll() == 0
+    kv, vv = R.slots_of(k, fmt, 192, kd), R.slots_of(v, fmt, 128, vd)
+    for s, n in enumerate(lens):
+        me, sl = torch.arange(n - q_len, n, device="cuda"), slice(s * q_len, (s + 1) * q_len)
+        R.Row(q[sl], R.pages_of(kv, table[s], n), R.pages_of(vv, table[s], n), torch.arange(n, device="cuda"), me, 1e7,
+              pos=me - (n - 1) + pos[s], p_step=2.0 ** -8 if fmt == BF16 else 2.0 ** -10).check(out[sl], lse[sl], f"sequence {s}")
