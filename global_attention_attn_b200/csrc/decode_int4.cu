@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode4_kernel(const __grid_co
     uint32_t off[4] = {0u, 0u, 0u, 0u};
     {
       float cs[2], sn[2];
-      const int pos0 = (p.positions ? p.positions[s] + 1 : ctx) - p.q_len;
+      const int pos0 = ctx - p.q_len;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         if (hf == 0 || draft[1] != draft[0]) {

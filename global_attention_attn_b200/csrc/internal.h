@@ -91,7 +91,7 @@ struct Decode4Params {
   const float* sink;
   const uint16_t* q;
   const int32_t* seq_lens;
-  const int32_t* positions;
+  const int32_t* positions;    // pages: rotary position of each sequence's last query token, or null
   int ring_slots;
   const uint8_t* k_cache;
   const uint8_t* v_cache;
