@@ -665,3 +665,77 @@ def test_decode_drafts_with_positions(fmt, q_len):
         me, sl = torch.arange(n - q_len, n, device="cuda"), slice(s * q_len, (s + 1) * q_len)
         R.Row(q[sl], R.pages_of(kv, table[s], n), R.pages_of(vv, table[s], n), torch.arange(n, device="cuda"), me, 1e7,
               pos=me - (n - 1) + pos[s], p_step=2.0 ** -8 if fmt == BF16 else 2.0 ** -10).check(out[sl], lse[sl], f"sequence {s}")
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [BF16, INT4])
+def test_eviction_step_captured(fmt):
+    """Append, decode, weights, selection and gather in one graph, replayed on other contents: bit for bit
+    what the calls give one by one."""
+    g, r = gen(29), np.random.default_rng(29)
+    lens, keep = [1500, 130, 900], 200
+    table, pages = R.table_of(lens, r)
+    table2, pages2 = R.table_of([keep] * 3, r)
+    k, v, _, _ = R.random_cache(fmt, pages, g)
+    fresh = _empty(fmt, pages2, 4)
+    state = dict(k=k, v=v, k2=fresh[0], v2=fresh[1], scores=torch.zeros((3, 4, 1500), device="cuda"),
+                 q=torch.zeros((3, 64, 192), device="cuda").bfloat16(), kn=torch.zeros((3, 4, 192), device="cuda").bfloat16(),
+                 vn=torch.zeros((3, 4, 128), device="cuda").bfloat16(), lens=R.i32([1, 1, 1]), pos=R.i32([0, 0, 0]))
+    seq = R.i32([0, 1, 2])
+
+    def step(t):
+        paged = dict(k_cache=t["k"], block_table=table, num_pages=pages, cache_dtype=fmt, rope_base=1e7)
+        M.mimo_kv_append(t["kn"], t["vn"], t["pos"], seq, cache_kind=PAGED, v_cache=t["v"], num_seqs=3, **paged)
+        kw = dict(max_seq_len=1500, num_kv_heads=4, **paged)
+        out, lse = M.mimo_attn_decode(t["q"], t["lens"], window=0, cache_kind=PAGED, v_cache=t["v"], **kw)
+        M.mimo_attn_weights(t["q"], lse, t["scores"], t["lens"], **kw)
+        idx, counts, kept = M.mimo_kv_select(t["scores"], t["lens"], max_seq_len=1500, keep=keep, recent=16, first=4)
+        M.mimo_kv_gather(t["k"], t["v"], table, t["k2"], t["v2"], table2, counts, num_kv_heads=4, num_pages=pages,
+                         num_pages_out=pages2, idx=idx, cache_dtype=fmt)
+        return out, lse, idx, counts, kept
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(state)
+    graph.replay()
+    for seed in (1, 2):
+        new = {n: torch.randn(state[n].shape, generator=gen(seed), device="cuda").bfloat16() for n in ("q", "kn", "vn")}
+        new.update(lens=R.i32(lens), pos=R.i32([n - 1 for n in lens]))
+        for n, t in new.items():
+            state[n].copy_(t)
+        alone = {n: t.clone() for n, t in state.items()}
+        graph.replay()
+        want = step(alone)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        for n in ("k", "v", "k2", "v2", "scores"):
+            assert torch.equal(state[n].view(torch.uint8), alone[n].view(torch.uint8))
+    assert M.status_poll() == 0
+
+
+@gpu
+@pytest.mark.parametrize("q_len", [1, 4])
+@pytest.mark.parametrize("lens", [[0, 4000, 0, 0, 77, 0], [300, 0, 0, 450, 0, 9]])
+def test_padded_batch_over_4_bits(lens, q_len):
+    """Rows of a batch that hold no sequence (length 0) are reported; the others are served."""
+    g, r = gen(31), np.random.default_rng(31)
+    table, pages = R.table_of(lens, r)
+    k, v, _, _ = R.random_cache(INT4, pages, g)
+    q = torch.randn((len(lens) * q_len, 64, 192), generator=g, device="cuda").bfloat16()
+    kw = dict(max_seq_len=max(lens), num_kv_heads=4, rope_base=1e7, k_cache=k, block_table=table, num_pages=pages,
+              cache_dtype=INT4, q_len=q_len)
+    out, lse = M.mimo_attn_decode(q, R.i32(lens), window=0, cache_kind=PAGED, v_cache=v, **kw)
+    assert M.status_poll() == M.MIMO_STATUS_BAD_INDEX
+    scores = torch.zeros((len(lens), 4, max(lens)), device="cuda")
+    M.mimo_attn_weights(q, lse, scores, R.i32(lens), **kw)
+    assert M.status_poll() == M.MIMO_STATUS_BAD_INDEX
+    kv, vv = R.slots_of(k, INT4, 192), R.slots_of(v, INT4, 128)
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert not scores[s].any()
+            continue
+        sl = slice(s * q_len, (s + 1) * q_len)
+        R.Row(q[sl], R.pages_of(kv, table[s], n), R.pages_of(vv, table[s], n), torch.arange(n, device="cuda"),
+              torch.arange(n - q_len, n, device="cuda"), 1e7).check(out[sl], lse[sl], f"sequence {s}")
+        # (as for a decode's own log-sum-exp: a KV head's 16 heads, for every draft)
+        assert float((scores[s].double().sum(-1) - 16 * q_len).abs().max()) < 16 * q_len * 2e-3
+    check_select(scores, lens, 100, 5)
