@@ -739,3 +739,45 @@ def test_padded_batch_over_4_bits(lens, q_len):
         # (as for a decode's own log-sum-exp: a KV head's 16 heads, for every draft)
         assert float((scores[s].double().sum(-1) - 16 * q_len).abs().max()) < 16 * q_len * 2e-3
     check_select(scores, lens, 100, 5)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [BF16, E4M3, INT4])
+def test_pages_beyond_four_gigabytes(fmt):
+    """The calls on the last pages of a large pool: bit for bit what they give on a small one."""
+    g, r = gen(32), np.random.default_rng(32)
+    lens = [700, 3, 129]
+    table, pages = R.table_of([n + 1 for n in lens], r)
+    k, v, kd, vd = R.random_cache(fmt, pages, g)
+    q = torch.randn((3, 64, 192), generator=g, device="cuda").bfloat16()
+    kn, vn = (torch.randn((3, 4, d), generator=g, device="cuda").bfloat16() for d in (192, 128))
+    table2, pages2 = R.table_of([100] * 3, r)
+    big = -(-(1 << 32) // (v[0].numel() * v.element_size())) + 50
+
+    def run(k, v, at, k2, v2, at2, n, n2):
+        t1, t2 = torch.where(table >= 0, table + at, table), table2 + at2
+        fm = dict(cache_dtype=fmt, k_dequant=kd)
+        M.mimo_kv_append(kn, vn, R.i32(lens), R.i32([0, 1, 2]), rope_base=1e7, cache_kind=PAGED, k_cache=k, v_cache=v,
+                         num_seqs=3, block_table=t1, num_pages=n, v_dequant=vd, **fm)
+        now = R.i32([x + 1 for x in lens])
+        kw = dict(max_seq_len=701, num_kv_heads=4, rope_base=1e7, k_cache=k, block_table=t1, num_pages=n, **fm)
+        out, lse = M.mimo_attn_decode(q, now, window=0, cache_kind=PAGED, v_cache=v, v_dequant=vd, **kw)
+        scores = torch.zeros((3, 4, 704), device="cuda")
+        M.mimo_attn_weights(q, lse, scores, now, **kw)
+        idx, counts, _ = M.mimo_kv_select(scores, now, max_seq_len=701, keep=100)
+        M.mimo_kv_gather(k, v, t1, k2, v2, t2, counts, num_kv_heads=4, num_pages=n, num_pages_out=n2, idx=idx, cache_dtype=fmt)
+        return out, lse, scores, idx
+    small, small2 = (k.clone(), v.clone()), _empty(fmt, pages2, 4)
+    want = run(*small, 0, *small2, 0, pages, pages2)
+    pool, pool2 = _empty(fmt, big, 4), _empty(fmt, big, 4)
+    for a, b in zip(pool, (k, v)):
+        a[big - pages:] = b
+    got = run(*pool, big - pages, *pool2, big - pages2, big, big)
+    assert M.status_poll() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for a, b, n in zip(pool + pool2, small + small2, (pages, pages, pages2, pages2)):
+        assert torch.equal(a[big - n:].view(torch.uint8), b.view(torch.uint8))
+        assert not a[:big - n].view(torch.uint8).any()
+    del pool, pool2
+    torch.cuda.empty_cache()
