@@ -165,8 +165,6 @@ int get_encoder(const char* fn, EncodeTiledFn* out) {
   return MIMO_OK;
 }
 
-// 3-D bf16 tensor [rows, heads, dim] (dim innermost) with box {64, box_h, box_rows},
-// 128-byte swizzle, zero fill out of bounds.
 int check_cache_dtype(const char* fn, int dtype, const float* kdq, const float* vdq) {
   if (dtype != MIMO_DTYPE_BF16 && dtype != MIMO_DTYPE_FP8_E4M3 && dtype != MIMO_DTYPE_INT4)
     return fail(MIMO_ERR_INVALID_ARG, "%s: unknown cache_dtype %d", fn, dtype);

@@ -14,10 +14,10 @@
 //     come from ldmatrix.trans: a 16-bit element of the transposed matrix is 4 dims of a key,
 //     so a register is 4 dims of a key pair, ready for the same masks;
 //   - the value offset is one more product per group of dims, p against a constant in the
-//     columns of that group (the groups share an accumulator).  A sum of p * code over tens of
-//     thousands of keys would grow far above the result and lose it to the accumulator's
-//     rounding; so the odd key of each pair enters as -p * (15 - code) (the complement is free
-//     in the mask's LOP3) and the sum stays near zero on the way;
+//     columns of that group (the groups share an accumulator).  Codes are never negative, so a sum of
+//     p * code over a ring's keys would be 8 times the weights' sum whatever the result, and the
+//     accumulator's rounding be relative to that; so the odd key of each pair enters as
+//     -p * (15 - code) (the complement is free in the mask's LOP3) and the sum stays near zero;
 //   - the rotated query dims enter as two fp16 terms: no 16-bit type holds them to the digits of
 //     an fp32 log-sum-exp.
 //
@@ -28,6 +28,10 @@
 // leader warp issues the copies of later tiles itself (one bulk copy for the codes and for the
 // scales, one TMA tile with the 64-byte swizzle for the values); there are no producer warps, so
 // all 8 warps multiply.
+//
+// 64 rings of 144 slots and 8 heads: 16.5 us, against 2.4 for the bytes.  Bound by latency: 1.8 warps
+// a scheduler, which issue in a third of the cycles (tensor pipe 13 %, ALU 26 %), walk a ring's five
+// tiles as two chains of dependent products.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -32,8 +32,11 @@
 // Measured (graph replay, in brackets the same on mma.sync with the drafts' rows in warps of their
 // own): 64 sequences of 4096..65536 keys, one token, 412 us (548), 3.7 TB/s, 0.57 of a copy's rate;
 // one of 131001 keys 39 us (64); one of 500 13.4 us (18.5); 16 of 1001..16384 with 1, 2, 4, 8
-// drafts 43, 62, 92 (160), 186 us.  Bound by the warps' instructions, 540 per warp and tile of
-// 16 columns (a third of them the unpacking): the copies alone take 260 us in the first call.
+// drafts 43, 62, 92 (160), 186 us.  Nothing is saturated (one token: the ALU pipe and the issue slots at
+// half; 4 drafts: 22 % and a third): a tile's chain of sums, vote, values and hand-over sets the pace,
+// 540 instructions per warp and tile of 16 columns (a third of them the unpacking) with four to five
+// warps a scheduler to cover its latencies, three with more columns.  The copies alone take 260 us in
+// the first call.
 // Short calls are the sum of what a worker does once: 2 us to its first tile's copy, 1.5 us for the
 // query operand, 3 us for the first tile (nothing overlaps yet, the references are set) and 1.5 us
 // for its rows.

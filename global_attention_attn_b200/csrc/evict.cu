@@ -330,7 +330,8 @@ __device__ __forceinline__ void widen_e4m3(const uint2& r, float sc, float* x) {
 // A block moves 32 slots of one destination page and KV head (128 left an SM one or two blocks
 // and their latencies at a few thousand slots: 13.8 us for 6750 of 4 heads widened), bound by the
 // bytes read and written: 16-byte pieces, neighbouring threads on neighbouring pieces of a row, several in
-// flight per thread.  SRC is the source's format; WIDE: the destination is bf16 (dims 0..63 of
+// flight per thread (16 x 4000 bf16 slots of 4 heads: 65 us, 5.0 TB/s, the warps waiting for their loads
+// alone).  SRC is the source's format; WIDE: the destination is bf16 (dims 0..63 of
 // a key fp16), and a thread makes 8 dims of it.
 template <int SRC, bool WIDE>
 __global__ void __launch_bounds__(kMoveThreads) gather_kernel(const __grid_constant__ GatherParams p) {

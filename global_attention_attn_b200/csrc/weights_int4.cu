@@ -14,8 +14,8 @@
 // The tensor memory is 96 columns of keys, 8 of a constant (the code offset's factor) and 6 x 64
 // of sums, all single: groups 0..2 and 3..5 run as two parts, so that the products of one run
 // behind the arithmetic on the other (three parts were a tenth slower, six two fifths).  What
-// bounds the kernel is instructions and the parts' handshakes, not the products and not the
-// copies (1.5 TB/s).  A ninth warp issues copies and products.
+// bounds the kernel is the chain of the parts' handshakes, which eight warps do not cover: no pipe is
+// above 36 % (1.5 TB/s).  A ninth warp issues copies and products.
 #include "int4_tc.cuh"
 #include "tiles.cuh"
 #include "../../include/mimoattn.h"
