@@ -47,8 +47,9 @@ __device__ __forceinline__ void rope_cos_sin(int pos, double inv_freq, float* c,
 }
 
 // The same with the reduced angle's rounding to fp32 put back (first order): half a step of the
-// results, not of the angle.  A code of a few bits turns on the digits that this keeps.
-__device__ __forceinline__ void rope_cos_sin_fine(int pos, double inv_freq, float* c, float* s) {
+// results, not of the angle.  A code of a few bits turns on the digits that this keeps.  Returns the
+// reduced angle.
+__device__ __forceinline__ double rope_cos_sin_fine(int pos, double inv_freq, float* c, float* s) {
   const double two_pi = 6.283185307179586476925286766559;
   const double theta = double(pos) * inv_freq;
   const double r = fma(-rint(theta * (1.0 / two_pi)), two_pi, theta);
@@ -57,6 +58,7 @@ __device__ __forceinline__ void rope_cos_sin_fine(int pos, double inv_freq, floa
   sincosf(rf, &sf, &cf);
   *c = fmaf(-sf, rest, cf);
   *s = fmaf(cf, rest, sf);
+  return r;
 }
 
 // OCP E4M3 (FP8) conversions.  Two floats -> two E4M3 bytes (round to nearest even,

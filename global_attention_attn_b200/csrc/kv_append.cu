@@ -115,22 +115,91 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
 }
 
 // 4-bit rows (int4.cuh): one warp per token and HPW of its KV heads, 640 bytes read and 180
-// written per head (6750 tokens of 4 heads: 14 us, 1.6 TB/s; bound by the quantising, 37 thread
-// instructions an element, most of them the border check below, on the half-rate ALU pipe: 58 % of it
-// busy).  A lane takes 8 dims at a time, so a group of 32 dims is four
+// written per head (6700 tokens of 4 heads: 14.1 us, 1.6 TB/s; bound by the quantising on the half-rate
+// ALU pipe).  A lane takes 8 dims at a time, so a group of 32 dims is four
 // neighbouring lanes, its largest magnitude two shuffles, and a lane's codes one word; the words of
 // four heads lie side by side (a head at a time left a quarter of the lanes idle in its key and
 // half in its value: 21 us).  Per group: scale = fp16(amax / 7), code = rint(x /
 // scale) + 8; 7 of amax keeps zero exact and both signs alike.  The rounding is the addition of
 // 1.5 * 2^23 + 8, whose low four bits are the code.  One bf16 element in 600 lies exactly between
 // two codes, where x * (1 / scale) may end on the wrong side: the remainder x - n * scale, which
-// is exact, says so (a division per element instead took twice the time).
+// is exact, says so (a division per element instead took twice the time); only words with a remainder
+// near half a step look at each of theirs.
 // All heads of a token turn by the same angles: with many tokens a warp takes four of them and
 // computes the angles once.
+// The rotated dims are fp32 sums, off by up to kSlip times the largest magnitude of their two groups.
+// Where that could move a scale (its fp16 rounding) or a code (its border), for one (token, four heads) in
+// some fifty, the warp does the word again with the rotation in 64 bits or two fp32 terms: codes and scales
+// are those of the exact one (of 5.4 M codes some tens were not; 0.3 us of the call above, 0.8 us of one with
+// 48 tokens where it happens).
 constexpr float kRound = 12582920.f;
+// x' = x c - y s: cos and sin are off by 1.25 x 2^-23 (sincosf by two units in the last place), the product
+// and the sum round by 2^-24 of themselves, and |x| + |y| is at most twice the larger of |x'|, |y'|:
+// 2 x 2.25 x 2^-23, of which this leaves a tenth.
+constexpr float kSlip = 0x1.4p-21f;
+
+// A word of a key (8 dims; a group of 32 is four neighbouring lanes) quantised from the exact rotation, by
+// the whole warp.  `turn`: this lane's dims are rotated ones; the partners' are four lanes away.  `angle`: that
+// of frequency `lane`, in [-pi, pi].  was: the word and the scale's bits, which stay in groups with an element
+// that is not finite.
+// (Two fp32 terms a value: with all of it in fp64 it took 1.4 us.)
+__device__ __noinline__ uint2 quantise_exact(uint4 raw, bool turn, double angle, float cap, int lane, uint2 was) {
+  // cos and sin by their Taylor series on [-pi/4, pi/4] (to 2^-41; fp64 steps take some 60 cycles each, so
+  // the sums are short chains)
+  const float turns = rintf(float(angle) * 0.636619772f);
+  const double r = fma(double(-turns), 1.5707963267948966, angle), q = r * r, q2 = q * q;
+  const double s5 = fma(q, 1.0 / 6227020800, -1.0 / 39916800), s3 = fma(q, 1.0 / 362880, -1.0 / 5040), s1 = fma(q, 1.0 / 120, -1.0 / 6);
+  const double c5 = fma(q, 1.0 / 479001600, -1.0 / 3628800), c3 = fma(q, 1.0 / 40320, -1.0 / 720), c1 = fma(q, 1.0 / 24, -0.5);
+  const double s = fma(r * q, fma(q2, fma(q2, s5, s3), s1), r), c = fma(q, fma(q2, fma(q2, c5, c3), c1), 1.0);
+  float sh = float(s), ch = float(c), sl = float(s - double(sh)), cl = float(c - double(ch));
+  const int quarter = int(turns) & 3;
+  if (quarter & 1) {
+    const float h = sh, l = sl;
+    sh = ch, sl = cl, ch = h, cl = l;
+  }
+  if (quarter >= 2) sh = -sh, sl = -sl;
+  if (quarter == 1 || quarter == 2) ch = -ch, cl = -cl;
+  float x[8], xl[8], amax = 0.f;  // values and what they leave over
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 2 ? raw.x : (i < 4 ? raw.y : (i < 6 ? raw.z : raw.w));
+    const float u = (i & 1) ? hi_bf16(w) : lo_bf16(w), v0 = __shfl_xor_sync(0xffffffffu, u, 4), v = (lane & 4) ? v0 : -v0;
+    const int from = 8 * (lane & 3) + i;
+    const float cih = __shfl_sync(0xffffffffu, ch, from), cil = __shfl_sync(0xffffffffu, cl, from);
+    const float sih = __shfl_sync(0xffffffffu, sh, from), sil = __shfl_sync(0xffffffffu, sl, from);
+    const float a = __fmul_rn(u, cih), b = __fmul_rn(v, sih), sum = __fadd_rn(a, b), part = __fsub_rn(sum, a);
+    const float rest = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, part)), __fsub_rn(b, part)) + (fmaf(u, cih, -a) + fmaf(v, sih, -b)) +
+                       fmaf(u, cil, v * sil);
+    x[i] = turn ? __fadd_rn(sum, rest) : u;
+    xl[i] = turn ? __fsub_rn(rest, __fsub_rn(x[i], sum)) : 0.f;
+    amax = fmaxf(amax, fabsf(x[i]));
+    bad = bad || !(fabsf(x[i]) < INFINITY);
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  float more = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) more = fabsf(x[i]) == amax ? fmaxf(more, x[i] > 0.f ? xl[i] : -xl[i]) : more;
+  more = fmaxf(more, __shfl_xor_sync(0xffffffffu, more, 1));
+  more = fmaxf(more, __shfl_xor_sync(0xffffffffu, more, 2));
+  const bool keep = (__ballot_sync(0xffffffffu, bad) >> (lane & 28)) & 15u;
+  const float want = float((double(amax) + double(more)) * (1.0 / 7.0));
+  const __half scale_h = __float2half_rn(fminf(want, cap));
+  const float scale = __half2float(scale_h), half = 0.5f * scale, inv = scale > 0.f ? __fdividef(1.f, scale) : 0.f;
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float n = rintf(fminf(fmaxf(x[i] * inv, -7.f), 7.f));
+    const float d = fmaf(-n, scale, x[i]), over = (fabsf(d) - half) + (d > 0.f ? xl[i] : -xl[i]);
+    if (inv > 0.f && (over > 0.f || (over == 0.f && (int(n) & 1)))) n += d > 0.f ? 1.f : -1.f;
+    word |= uint32_t(int(fminf(fmaxf(n, -7.f), 7.f)) + 8) << (4 * i);
+  }
+  return keep ? was : make_uint2(word, __float_as_uint(scale));
+}
 
 template <int HPW>
-__global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, 3) kv_append_int4_kernel(const AppendParams p) {
   const int warp = int((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
   const int lane = threadIdx.x & 31;
   const int parts = p.hkv / HPW;
@@ -150,8 +219,9 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams 
     }
   };
   bool range = false;
-  // 8 dims of a group -> their word of codes; every lane of the warp takes part
-  auto quantise = [&](float* x, float cap, float& scale) -> uint32_t {
+  // 8 dims of a group -> their word of codes; every lane of the warp takes part.  turned: the dims are
+  // rotated, and `near` tells whether what that is off by could matter.
+  auto quantise = [&](float* x, float cap, float& scale, bool turned, bool& near) -> uint32_t {
     float amax = 0.f;
     bool bad = false;
 #pragma unroll
@@ -164,20 +234,36 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams 
     const float want = float(double(amax) * (1.0 / 7.0));  // (a float divided by 7, rounded once but for one case in 2^28)
     scale = __half2float(__float2half_rn(fminf(want, cap)));
     range = range || bad || want > cap;
+    const float slip = turned ? kSlip * fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4)) : 0.f;
+    if (turned) {
+      // (a seventh of it, and a step of `want` itself)
+      const float e = 0.15f * slip + 0x1p-23f * want;
+      near = __half_as_ushort(__float2half_rn(want - e)) != __half_as_ushort(__float2half_rn(want + e));
+    }
     if (bad || want > 1.05f * scale) {  // (a scale cut to its range, or a subnormal one: quotients beyond 7.5)
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -7.f * scale), 7.f * scale);
     }
     const float inv = scale > 0.f ? __fdividef(1.f, scale) : 0.f, half = 0.5f * scale;
     uint32_t w = 0;
+    float dmax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float sum = x[i] * inv + kRound, n = sum - kRound;
-      const float d = fmaf(-n, scale, x[i]);
-      const bool off = fabsf(d) > half || (fabsf(d) == half && (__float_as_uint(sum) & 1u));
-      const uint32_t code = __float_as_uint(sum) + (off ? (d > 0.f ? 1u : ~0u) : 0u);
-      w |= (code & 15u) << (4 * i);
+      const float sum = x[i] * inv + kRound;
+      dmax = fmaxf(dmax, fabsf(fmaf(kRound - sum, scale, x[i])));
+      w |= (__float_as_uint(sum) & 15u) << (4 * i);
     }
+    if (dmax >= 0.99999f * half) {
+      w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float sum = x[i] * inv + kRound, d = fmaf(kRound - sum, scale, x[i]);
+        const bool off = fabsf(d) > half || (fabsf(d) == half && (__float_as_uint(sum) & 1u));
+        const uint32_t code = __float_as_uint(sum) + (off ? (d > 0.f ? 1u : ~0u) : 0u);
+        w |= (code & 15u) << (4 * i);
+      }
+    }
+    if (turned) near = near || (scale > 0.f && dmax + slip >= 0.999999f * half);  // (no scale, no codes)
     return w;
   };
   // the heads' words of 8 dims side by side, 32 at a time: word m is word m % 24 of key m / 24, or
@@ -199,7 +285,7 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams 
   // words 0..3 of a key hold dims 8 w + i, words 4..7 their partners + 32: x' = x c -+ y s.  24 and 32
   // are multiples of 8, so partners are four lanes apart whatever the head
   float c, sn, ci[8], si[8];
-  rope_cos_sin_fine(pos, p.rope.inv_freq[lane], &c, &sn);
+  const double angle = rope_cos_sin_fine(pos, p.rope.inv_freq[lane], &c, &sn);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     ci[i] = __shfl_sync(0xffffffffu, c, 8 * (lane & 3) + i);
@@ -217,7 +303,14 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams 
       const float y = __shfl_xor_sync(0xffffffffu, x[e], 4);
       if (w < 8) x[e] = x[e] * ci[e] + y * si[e];
     }
-    const uint32_t word = quantise(x, kF16Max, scale);
+    bool near = false;
+    uint32_t word = quantise(x, kF16Max, scale, true, near);
+    near = near && w < 8 && m < 24 * HPW;
+    if (__any_sync(0xffffffffu, near)) {
+      const uint2 e = quantise_exact(kr[i], w < 8, angle, kF16Max, lane, make_uint2(word, __float_as_uint(scale)));
+      word = e.x;
+      scale = __uint_as_float(e.y);
+    }
     if (m < 24 * HPW) {
       uint8_t* const kb = reinterpret_cast<uint8_t*>(p.k_cache) + (block0 + h) * (long(slots) * kI4KSlot);
       reinterpret_cast<uint32_t*>(kb + long(slot) * kI4KCodes)[(w & 3) * 6 + (w >> 2)] = word;
@@ -230,7 +323,8 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(const AppendParams 
     const int m = 32 * i + lane, h = m / 16, w = m % 16;
     float x[8], scale;
     widen(vr[i], x);
-    const uint32_t word = quantise(x, kI4VScaleMax, scale);
+    bool near;
+    const uint32_t word = quantise(x, kI4VScaleMax, scale, false, near);
     if (m < 16 * HPW) {
       uint8_t* const vb = reinterpret_cast<uint8_t*>(p.v_cache) + (block0 + h) * (long(slots) * kI4VSlot);
       reinterpret_cast<uint32_t*>(vb + long(slot) * kI4VCodes)[w] = word;

@@ -133,7 +133,8 @@ MIMO_API int mimo_window_from_left_right(int left, int right, int* window);
  *     and 64 bytes), then its S rows of scales (6 and 4 fp16).  Byte i of a row of codes holds
  *     dims 2i (low four bits) and 2i + 1; a key row's 24 words of 8 dims are stored as word w
  *     at (w % 4) * 6 + w / 4.  An append stores scale = fp16(amax / 7) of the group's largest
- *     magnitude amax (fp32 quotient) and code = 8 + rint(x / scale), -7 <= code - 8 <= 7; a
+ *     magnitude amax (fp32 quotient) and code = 8 + rint(x / scale), -7 <= code - 8 <= 7, x the
+ *     exactly rotated element (not its fp32 value, which may lie across a border); a
  *     scale beyond 65504 (keys) or 1023 (values) is stored as that limit, an element that is
  *     not finite as +-7 (MIMO_STATUS_RANGE).  Codes and scales made elsewhere are read as
  *     they are (code 0 too); value scales must not pass 1023 in magnitude. */

@@ -652,3 +652,59 @@ def test_decode_noalloc_drafts_and_positions(fmt):
         want = M.mimo_attn_decode(q, R.i32(lens), **kw)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert M.status_poll() == 0
+
+
+@gpu
+@pytest.mark.parametrize("tokens, calls", [(20000, 2), (400, 60)])
+@pytest.mark.parametrize("base, hkv", [(1e7, 4), (1e4, 8)])
+def test_append_codes_of_the_exact_rotation(tokens, calls, base, hkv):
+    """Every code and scale is the rule's on the rotation in 64 bits, also where a quotient or a scale lies
+    next to a border (a rotation in fp32 moves some tens of 5 million codes)."""
+    g, r = gen(80), np.random.default_rng(80)
+    blocks = -(-tokens // 128)
+    table = R.i32(r.permutation(blocks)[None])
+    seq, slots = torch.zeros(tokens, dtype=torch.int32, device="cuda"), R.i32(np.arange(tokens))
+
+    def rule(x):
+        x = x.unflatten(-1, (-1, 32))
+        s = (x.abs().amax(-1) / 7).float().half().double()[..., None]
+        n = torch.where(s > 0, torch.round(x / s).clamp(-7, 7), torch.zeros_like(x))
+        return (n * s).flatten(-2)
+    for _ in range(calls):
+        kn = torch.randn((tokens, hkv, 192), generator=g, device="cuda").mul_(2).bfloat16()
+        vn = torch.randn((tokens, hkv, 128), generator=g, device="cuda").bfloat16()
+        pos = R.i32(r.integers(0, 131072, tokens))
+        k, v = M.empty_int4_cache(blocks, hkv)
+        _append(kn, vn, pos, seq, k, v, base, cache_kind=PAGED, num_seqs=1, block_table=table, num_pages=blocks, slots=slots)
+        got = R.pages_of(R.slots_of(k, R.INT4, 192), table[0], tokens).transpose(0, 1)
+        assert torch.equal(got, rule(R.rotate(kn, pos, base)))
+        got = R.pages_of(R.slots_of(v, R.INT4, 128), table[0], tokens).transpose(0, 1)
+        assert torch.equal(got, rule(vn.double()))
+    assert M.status_poll() == 0
+
+
+@gpu
+def test_append_not_finite_beside_other_groups():
+    """NaN and infinities in a key: +-7 of their group as the rule says, whatever the words beside them."""
+    g = gen(81)
+    n = 3000
+    kn = torch.randn((n, 4, 192), generator=g, device="cuda").bfloat16()
+    vn = torch.randn((n, 4, 128), generator=g, device="cuda").bfloat16()
+    kn[::3, 1, 5], kn[1::3, 2, 40], kn[2::3, 0, 100] = float("inf"), float("nan"), -float("inf")
+    k, v = M.empty_int4_cache(24, 4)
+    pos = R.i32(np.arange(n))
+    _append(kn, vn, pos, torch.zeros_like(pos), k, v, 1e7, cache_kind=PAGED, num_seqs=1, block_table=R.i32(np.arange(24)[None]),
+            num_pages=24)
+    assert M.status_poll() == M.MIMO_STATUS_RANGE
+    got = R.pages_of(R.slots_of(k, R.INT4, 192), R.i32(np.arange(24)), n).transpose(0, 1)
+    assert torch.isfinite(got).all()
+    assert (got[2::3, 0, 100] == -7 * 65504).all() and (got[2::3, 0, 96:100] == 0).all()
+    # (dims 5 and 37, 40 and 8 turn together; a NaN takes no part in its group's scale)
+    want = R.rotate(kn, pos, 1e7)
+    clean = torch.isfinite(want.unflatten(-1, (-1, 32))).all(-1)
+    ref = want.unflatten(-1, (-1, 32))
+    s = (ref.abs().amax(-1) / 7).float().half().double()[..., None]
+    ref = torch.round(ref / s).clamp(-7, 7) * s
+    assert torch.equal(got.unflatten(-1, (-1, 32))[clean], ref[clean])
+    bad = ~torch.isfinite(want)
+    assert bad.any() and (got[bad] != 0).all()
