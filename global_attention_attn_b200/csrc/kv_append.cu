@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
 }
 
 // 4-bit rows (int4.cuh): one warp per token and HPW of its KV heads, 640 bytes read and 180
-// written per head (6700 tokens of 4 heads: 14.1 us, 1.6 TB/s; bound by the quantising on the half-rate
-// ALU pipe).  A lane takes 8 dims at a time, so a group of 32 dims is four
+// written per head (6700 tokens of 4 heads: 14.1 us, 1.6 TB/s; bound by the quantising, 30 thread
+// instructions an element, half of the ALU pipe and 59 % of the issue slots).  A lane takes 8 dims at a time, so a group of 32 dims is four
 // neighbouring lanes, its largest magnitude two shuffles, and a lane's codes one word; the words of
 // four heads lie side by side (a head at a time left a quarter of the lanes idle in its key and
 // half in its value: 21 us).  Per group: scale = fp16(amax / 7), code = rint(x /
